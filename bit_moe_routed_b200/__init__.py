@@ -10,6 +10,7 @@ if the library is missing or the device is not sm_100, calls raise.
     y, y_sh = expert_ffn(x, k, weights, offsets, perm)  # steps 3-7 (FP4 x FP8 FFN)
     out = combine(y, y_sh, w, pos)              # step 8
     r = forward(x, scores, k, weights)          # all of it in one call (one kernel at T=1)
+    r = forward_w4(x, scores, k, layer)         # the layer on 4-bit weights with group scales
 """
 from __future__ import annotations
 
@@ -42,6 +43,7 @@ EXPORTS = (
     "moe_fp8_gemm", "moe_fp8_gemm_workspace_size", "moe_shared_expert_fp8",
     "moe_shared_expert_fp8_workspace_size", "moe_shared_expert_fp8_offsets",
     "moe_expert_cache_reset", "moe_forward_streamed",
+    "moe_w4_gemm", "moe_forward_w4", "moe_w4_workspace_size",
 )
 
 
@@ -60,6 +62,15 @@ class _Fp8Expert(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "gate", "gate_scales", "up", "up_scales", "down", "down_scales")] + [
         ("d", ctypes.c_int), ("f", ctypes.c_int)]
+
+
+class _W4Matrix(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "zeros")]
+
+
+class _W4Weights(ctypes.Structure):
+    _fields_ = [(n, _W4Matrix) for n in ("gate", "up", "down")] + [
+        (n, ctypes.c_int) for n in ("E", "d", "f", "group", "dtype", "shared")]
 
 
 class _Weights(ctypes.Structure):
@@ -119,6 +130,9 @@ def lib():
             "moe_forward_streamed": [P, P, I, ctypes.POINTER(_HostExperts),
                                      ctypes.POINTER(_ExpertCache), P, P, P, P, P, P, P, P, P,
                                      P, Z, P],
+            "moe_w4_gemm": [P, I, I, ctypes.POINTER(_W4Matrix), I, I, I, P, P],
+            "moe_forward_w4": [P, P, I, I, ctypes.POINTER(_W4Weights), P, P, P, P, Z, P],
+            "moe_w4_workspace_size": [I, I, I, I, I, I],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -128,6 +142,7 @@ def lib():
         L.moe_dispatch_workspace_size.restype = ctypes.c_size_t
         L.moe_fp8_gemm_workspace_size.restype = ctypes.c_size_t
         L.moe_shared_expert_fp8_workspace_size.restype = ctypes.c_size_t
+        L.moe_w4_workspace_size.restype = ctypes.c_size_t
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -385,6 +400,126 @@ def forward_streamed(x: torch.Tensor, scores: torch.Tensor, k: int, host: HostEx
                                       _stream(stream)))
     return dict(idx=o["idx"], w=o["w"], counts=o["counts"], offsets=o["offsets"],
                 perm=o["perm"], pos=o["pos"], y=o["y"], y_shared=o["y_shared"], out=o["out"])
+
+
+_DTYPE16 = {torch.bfloat16: 0, torch.float16: 1}  # MOE_BF16, MOE_F16
+
+
+class W4Matrix:
+    """A matrix of 4-bit weights with group scales, or several of one shape: codes
+    [..., N, K/2] uint8 (low nibble = even element), scales [..., N, K/G] bf16 or fp16 with
+    G = 32, 64 or 128, zeros [..., N, K/G] uint8 (0..127) or None for 8 everywhere;
+    W = (code - zero) * scale.  The tensors are kept, not copied."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor,
+                 zeros: torch.Tensor | None = None):
+        if codes.dim() < 2 or codes.dtype != torch.uint8:
+            raise ValueError("codes must be uint8 [..., N, K/2]")
+        if scales.dtype not in _DTYPE16:
+            raise ValueError("scales must be bfloat16 or float16")
+        self.N, self.K = codes.shape[-2], 2 * codes.shape[-1]
+        if scales.shape[:-1] != codes.shape[:-1] or scales.shape[-1] < 1 or \
+                self.K % scales.shape[-1]:
+            raise ValueError("scales must be [..., N, K/G] beside codes [..., N, K/2]")
+        self.group = self.K // scales.shape[-1]
+        if self.group not in (32, 64, 128):
+            raise ValueError(f"group size {self.group} is not 32, 64 or 128")
+        if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+            raise ValueError("zeros must be uint8 with the shape of scales")
+        if any(t is not None and t.device != codes.device for t in (scales, zeros)):
+            raise ValueError("codes, scales and zeros must be on one device")
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.dtype, self.device = scales.dtype, codes.device
+
+    def struct(self) -> _W4Matrix:
+        return _W4Matrix(_p(self.codes), _p(self.scales), _p(self.zeros))
+
+
+class W4Layer:
+    """One layer's 4-bit weights: gate, up [n, f, d] and down [n, d, f] as W4Matrix, n = E
+    routed experts plus, with `shared`, the shared expert as the last."""
+
+    def __init__(self, gate: W4Matrix, up: W4Matrix, down: W4Matrix, shared: bool = True):
+        shape = gate.codes.shape
+        if len(shape) != 3 or up.codes.shape != shape or down.codes.dim() != 3 or \
+                down.codes.shape[0] != shape[0] or (down.N, down.K) != (gate.K, gate.N):
+            raise ValueError("gate and up must be [n, f, d], down [n, d, f]")
+        for m in (up, down):
+            if (m.group, m.dtype, m.device, m.zeros is None) != \
+                    (gate.group, gate.dtype, gate.device, gate.zeros is None):
+                raise ValueError("the matrices must share group size, type, device and having "
+                                 "zero points")
+        self.gate, self.up, self.down, self.shared = gate, up, down, bool(shared)
+        self.E, self.f, self.d = shape[0] - int(self.shared), gate.N, gate.K
+        if self.E < 1:
+            raise ValueError("no routed expert")
+        self.group, self.dtype, self.device = gate.group, gate.dtype, gate.device
+
+    def struct(self) -> _W4Weights:
+        return _W4Weights(self.gate.struct(), self.up.struct(), self.down.struct(), self.E, self.d,
+                          self.f, self.group, _DTYPE16[self.dtype], int(self.shared))
+
+
+def _check_on(device, **tensors) -> None:
+    """Tensors (name=(tensor, shape, dtype)) on `device`, which is the current one."""
+    for name, (t, shape, dtype) in tensors.items():
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the weights on {device}")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the weights' device {device} is not the current CUDA device")
+
+
+def w4_gemm(x: torch.Tensor, w: W4Matrix, out: torch.Tensor | None = None, stream=None):
+    """C [M, N] fp32 = x [M, K] (bf16 or fp16, the scales' type; M <= 64) times W [N, K]
+    transposed, W a 4-bit matrix with group scales (moe_w4_gemm)."""
+    if w.codes.dim() != 2:
+        raise ValueError("w4_gemm takes one matrix [N, K]")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M = x.shape[0]
+    if out is None:
+        out = torch.empty((M, w.N), dtype=torch.float32, device=x.device)
+    _check_on(w.device, x=(x, (M, w.K), w.dtype), out=(out, (M, w.N), torch.float32))
+    st = w.struct()
+    _check(lib().moe_w4_gemm(_p(x), _DTYPE16[w.dtype], M, ctypes.byref(st), w.N, w.K, w.group,
+                             _p(out), _stream(stream)))
+    return out
+
+
+def workspace_size_w4(T: int, k: int, w: W4Layer) -> int:
+    return int(lib().moe_w4_workspace_size(T, k, w.E, w.d, w.f, int(w.shared)))
+
+
+def alloc_workspace_w4(T: int, k: int, w: W4Layer) -> torch.Tensor:
+    """A workspace for forward_w4 with up to T tokens (calls that overlap on the GPU need one
+    each)."""
+    return torch.empty(max(workspace_size_w4(T, k, w), 256), dtype=torch.uint8, device=w.device)
+
+
+def forward_w4(x: torch.Tensor, scores: torch.Tensor, k: int, w: W4Layer,
+               ws: torch.Tensor | None = None, stream=None, outs: dict | None = None):
+    """The whole layer on 4-bit weights for up to 64 tokens (moe_forward_w4, two kernels);
+    returns {idx, w, out}.  `outs` may hold preallocated outputs under the same names."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    T = x.shape[0]
+    if ws is None:
+        ws = alloc_workspace_w4(T, k, w)
+    o = dict(outs) if outs is not None else {}
+    shapes = {"idx": ((T, k), torch.int32), "w": ((T, k), torch.float32),
+              "out": ((T, w.d), torch.float32)}
+    for name, (shape, dtype) in shapes.items():
+        if name not in o:
+            o[name] = torch.empty(shape, dtype=dtype, device=x.device)
+    _check_on(w.device, x=(x, (T, w.d), w.dtype), scores=(scores, (T, w.E), torch.float32),
+              ws=(ws, ws.shape, torch.uint8), **{n: (o[n], *shapes[n]) for n in shapes})
+    st = w.struct()
+    _check(lib().moe_forward_w4(_p(scores), _p(x), T, k, ctypes.byref(st), _p(o["idx"]),
+                                _p(o["w"]), _p(o["out"]), _p(ws), ws.numel(), _stream(stream)))
+    return dict(idx=o["idx"], w=o["w"], out=o["out"])
 
 
 def set_wait_limit_ns(n: int) -> None:

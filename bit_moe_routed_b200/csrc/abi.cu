@@ -944,6 +944,127 @@ int moe_shared_expert_fp8(const uint16_t* x_bf16, int T, const moe_fp8_expert_t*
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "shared expert fp8 launch");
 }
 
+namespace {
+
+int check_w4_matrix(const moe_w4_matrix_t& m) {
+  if (!m.codes || !m.scales) return fail(MOE_ERR_INVALID_ARG, "a 4-bit weight pointer is NULL");
+  if (!aligned(m.codes, 16) || !aligned(m.scales, 2))
+    return fail(MOE_ERR_INVALID_ARG, "codes must be 16-byte aligned, scales 2-byte aligned");
+  return MOE_OK;
+}
+int check_w4_format(int group, int dtype) {
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "group=%d is not 32, 64 or 128", group);
+  if (dtype != MOE_BF16 && dtype != MOE_F16)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d is not MOE_BF16 or MOE_F16", dtype);
+  return MOE_OK;
+}
+bool w4_sizes_ok(int T, int k, int E, int d, int f, int shared) {
+  return T >= 0 && T <= 64 && E >= 1 && E <= 1024 && k >= 1 && k <= E && k <= 32 && d >= 32 &&
+         d <= 16384 && d % 32 == 0 && f >= 32 && f <= 16384 && f % 32 == 0 &&
+         (shared == 0 || shared == 1);
+}
+
+}  // namespace
+
+int moe_w4_gemm(const void* x, int dtype, int M, const moe_w4_matrix_t* w, int N, int K,
+                int group, float* C, void* stream) {
+  if (!w) return fail(MOE_ERR_INVALID_ARG, "NULL weights");
+  if (M < 0 || M > 64) return fail(MOE_ERR_INVALID_ARG, "M=%d outside [0, 64]", M);
+  int rc = check_w4_format(group, dtype);
+  if (rc) return rc;
+  if (N < 1 || N > (1 << 24)) return fail(MOE_ERR_INVALID_ARG, "N=%d outside [1, 2^24]", N);
+  if (K < group || K % group || K > (1 << 20))
+    return fail(MOE_ERR_INVALID_ARG, "K=%d must be a multiple of group=%d, at most 2^20", K, group);
+  if (M == 0) return MOE_OK;
+  rc = check_w4_matrix(*w);
+  if (rc) return rc;
+  if (!x || !C) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(x, 16) || !aligned(C, 4))
+    return fail(MOE_ERR_INVALID_ARG, "x must be 16-byte aligned, C 4-byte aligned");
+  DeviceInfo di;
+  rc = device_info(di);
+  if (rc) return rc;
+  W4GemmLaunch a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.codes = w->codes;
+  a.scales = w->scales;
+  a.zeros = w->zeros;
+  a.C = C;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.group = group;
+  a.f16 = dtype == MOE_F16;
+  cudaError_t e = launch_w4_gemm(a, static_cast<cudaStream_t>(stream), di.sms);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "w4_gemm launch");
+}
+
+size_t moe_w4_workspace_size(int T, int k, int E, int d, int f, int shared) {
+  if (!w4_sizes_ok(T, k, E, d, f, shared)) return 0;
+  return w4_layer_layout(T, k, shared, d, f).total;
+}
+
+int moe_forward_w4(const float* scores, const void* x, int T, int k, const moe_w4_weights_t* w,
+                   int32_t* topk_idx, float* topk_w, float* out, void* ws, size_t ws_bytes,
+                   void* stream) {
+  if (!w) return fail(MOE_ERR_INVALID_ARG, "NULL weights");
+  if (T < 0 || T > 64) return fail(MOE_ERR_INVALID_ARG, "T=%d outside [0, 64]", T);
+  int rc = check_w4_format(w->group, w->dtype);
+  if (rc) return rc;
+  if (!w4_sizes_ok(T, k, w->E, w->d, w->f, w->shared) || w->d % w->group || w->f % w->group)
+    return fail(MOE_ERR_INVALID_ARG,
+                "k=%d, E=%d, d=%d, f=%d, shared=%d: k in [1, min(E, 32)], E in [1, 1024], d and f "
+                "multiples of group=%d in [32, 16384], shared 0 or 1",
+                k, w->E, w->d, w->f, w->shared, w->group);
+  if (T == 0) return MOE_OK;
+  const moe_w4_matrix_t* ms[3] = {&w->gate, &w->up, &w->down};
+  for (const moe_w4_matrix_t* m : ms) {
+    rc = check_w4_matrix(*m);
+    if (rc) return rc;
+    if ((m->zeros == nullptr) != (w->gate.zeros == nullptr))
+      return fail(MOE_ERR_INVALID_ARG, "zero points must be given for all three matrices or none");
+  }
+  if (!scores || !x || !topk_idx || !topk_w || !out) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(scores, 4) || !aligned(x, 16) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+      !aligned(out, 16))
+    return fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned, the rest 4-byte aligned");
+  if (!ws || !aligned(ws, 256))
+    return fail(MOE_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  const size_t need = w4_layer_layout(T, k, w->shared, w->d, w->f).total;
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  DeviceInfo di;
+  rc = device_info(di);
+  if (rc) return rc;
+  W4LayerLaunch a{};
+  a.scores = scores;
+  a.x = static_cast<const uint16_t*>(x);
+  a.gate_codes = w->gate.codes;
+  a.gate_scales = w->gate.scales;
+  a.gate_zeros = w->gate.zeros;
+  a.up_codes = w->up.codes;
+  a.up_scales = w->up.scales;
+  a.up_zeros = w->up.zeros;
+  a.down_codes = w->down.codes;
+  a.down_scales = w->down.scales;
+  a.down_zeros = w->down.zeros;
+  a.idx = topk_idx;
+  a.w_out = topk_w;
+  a.out = out;
+  a.ws = static_cast<uint8_t*>(ws);
+  a.T = T;
+  a.k = k;
+  a.E = w->E;
+  a.d = w->d;
+  a.f = w->f;
+  a.group = w->group;
+  a.shared = w->shared;
+  a.f16 = w->dtype == MOE_F16;
+  cudaError_t e = launch_w4_layer(a, static_cast<cudaStream_t>(stream), di.sms);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "4-bit layer launch");
+}
+
 int moe_expert_cache_reset(const moe_expert_cache_t* c, void* stream) {
   if (!c || !c->slot_of || !c->expert_of || !c->last_use || !c->clock || !c->stats || !c->fetch)
     return fail(MOE_ERR_INVALID_ARG, "NULL cache pointer");

@@ -261,6 +261,35 @@ struct Fp8Launch {
 size_t fp8_gemm_ws_bytes(int M, int N, int K, bool fused);
 size_t fp8_gemm_counters(int N, bool fused);  // counters (ints) a launch uses
 cudaError_t launch_fp8_gemm(const Fp8Launch& a, cudaStream_t s);
+// 4-bit weights with group scales (w4_gemm.cu, w4_layer.cu): codes [N][K/2], scales [N][K/G]
+// in the activations' type (f16: fp16, else bf16), zeros [N][K/G] or NULL.
+struct W4GemmLaunch {
+  const uint16_t* x;  // [M][K]
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  float* C;           // [M][N]
+  int M, N, K, group;
+  bool f16;
+};
+cudaError_t launch_w4_gemm(const W4GemmLaunch& a, cudaStream_t s, int num_sms);
+struct W4LayerLaunch {
+  const float* scores;
+  const uint16_t* x;
+  const uint8_t *gate_codes, *up_codes, *down_codes;
+  const void *gate_scales, *up_scales, *down_scales;
+  const uint8_t *gate_zeros, *up_zeros, *down_zeros;
+  int32_t* idx;
+  float *w_out, *out;
+  uint8_t* ws;
+  int T, k, E, d, f, group, shared;
+  bool f16;
+};
+struct W4LayerLayout {
+  size_t hh, hl, y, cnt, total;
+};
+W4LayerLayout w4_layer_layout(int T, int k, int shared, int d, int f);
+cudaError_t launch_w4_layer(const W4LayerLaunch& a, cudaStream_t s, int num_sms);
 // Expert cache (stream.cu): the LRU decisions of one token's step (one thread) and the
 // copy of the listed experts from host memory into their slots.  fetch = [count, then
 // (expert, slot) pairs]; stats = [hits, misses] accumulated.

@@ -266,6 +266,66 @@ int moe_shared_expert_fp8_offsets(int T, int d, int f, size_t off[5]);
 int moe_shared_expert_fp8(const uint16_t* x_bf16, int T, const moe_fp8_expert_t* w,
                           float* y_shared, void* ws, size_t ws_bytes, void* stream);
 
+/* 4-bit weights with group scales: the integer 4-bit format of quantised checkpoints, beside
+ * the FP4 and 2-bit codecs above (ai-muninn.com post "一張 22G 老卡跑 284B": decode is bound by
+ * reading the weights, so few bits a weight are what makes it fast; the pages fix no such
+ * layout, this library's is below).  A matrix of N rows over a reduction of K elements in
+ * groups of G = 32, 64 or 128:
+ *   codes  [N][K/2] uint8, two codes q per byte (low nibble = even element); 16-byte aligned
+ *   scales [N][K/G] bf16 or fp16, the activations' type; 2-byte aligned
+ *   zeros  [N][K/G] uint8, 0..127 (the low seven bits are read), or NULL: 8 everywhere
+ *   W[n][k] = (q[n][k] - zeros[n][k/G]) * scales[n][k/G].
+ * Activations stay in 16 bits: products are exact, a group's sum and everything after it is
+ * fp32. */
+typedef struct {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+} moe_w4_matrix_t;
+
+#define MOE_BF16 0
+#define MOE_F16 1
+
+/* C[m][n] = sum_k x[m][k] W[n][k] for a decode-sized batch (moe_fp8_gemm's counterpart for
+ * 4-bit weights and 16-bit activations).
+ *   x [M][K] bf16 or fp16 bit patterns (`dtype`; the scales have the same type), 16-byte
+ *   aligned; C [M][N] fp32 out, 4-byte aligned.
+ * 0 <= M <= 64; K a positive multiple of group, at most 2^20; 1 <= N <= 2^24.  One kernel, no
+ * workspace.  Rows of x do not meet: a row's result does not depend on the others. */
+int moe_w4_gemm(const void* x, int dtype, int M, const moe_w4_matrix_t* w, int N, int K,
+                int group, float* C, void* stream);
+
+/* One layer's 4-bit weights, E routed experts and, with `shared`, a shared one (index E),
+ * contiguous per matrix: gate, up [E + shared][f][d], down [E + shared][d][f].  Either all
+ * three matrices have zero points or none.  d and f: multiples of group, 32..16384. */
+typedef struct {
+  moe_w4_matrix_t gate;
+  moe_w4_matrix_t up;
+  moe_w4_matrix_t down;
+  int E;
+  int d;
+  int f;
+  int group;
+  int dtype;
+  int shared;
+} moe_w4_weights_t;
+
+/* moe_forward on 4-bit weights with group scales, for a few tokens, in two kernels: the top-k
+ * of the scores, g = W_gate x, u = W_up x, h = silu(g) * u, y = W_down h for every selected
+ * expert and the shared one, and out[t] = y_shared[t] + sum_j topk_w[t,j] y[t,j].
+ *   scores, topk_idx, topk_w, out as for moe_forward; x [T][d] of w->dtype, 16-byte aligned.
+ *   ws: at least moe_w4_workspace_size(T, k, E, d, f, shared) bytes, 256-byte aligned; its
+ *   contents need not be initialised.  Calls that may overlap on the GPU (other streams,
+ *   graphs replayed side by side) need a workspace each.
+ * 0 <= T <= 64; 1 <= k <= min(E, 32); 1 <= E <= 1024.  h passes between the kernels as two
+ * bf16 terms (16 significant bits).  A call is deterministic. */
+int moe_forward_w4(const float* scores, const void* x, int T, int k, const moe_w4_weights_t* w,
+                   int32_t* topk_idx, float* topk_w, float* out, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/* Bytes of workspace moe_forward_w4 needs (0 on sizes it rejects). */
+size_t moe_w4_workspace_size(int T, int k, int E, int d, int f, int shared);
+
 /* Expert streaming (NEXT-4, one GPU): routed experts that live in host memory
  * ([P1] "DeepSeek-V4-Flash的可能性": routed experts in host RAM, the shared expert and
  * attention resident; [P2] "核心实现一": experts streamed in as they are needed, kept
