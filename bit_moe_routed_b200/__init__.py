@@ -409,7 +409,8 @@ class W4Matrix:
     """A matrix of 4-bit weights with group scales, or several of one shape: codes
     [..., N, K/2] uint8 (low nibble = even element), scales [..., N, K/G] bf16 or fp16 with
     G = 32, 64 or 128, zeros [..., N, K/G] uint8 (0..127) or None for 8 everywhere;
-    W = (code - zero) * scale.  The tensors are kept, not copied."""
+    W = (code - zero) * scale.  The tensors, contiguous, are kept, not copied; what they hold
+    may change, which tensors they are may not."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor,
                  zeros: torch.Tensor | None = None):
@@ -430,9 +431,11 @@ class W4Matrix:
             raise ValueError("codes, scales and zeros must be on one device")
         self.codes, self.scales, self.zeros = codes, scales, zeros
         self.dtype, self.device = scales.dtype, codes.device
+        self._struct = _W4Matrix(_p(codes), _p(scales), _p(zeros))
+        self._dtype_code, self._one = _DTYPE16[self.dtype], codes.dim() == 2
 
     def struct(self) -> _W4Matrix:
-        return _W4Matrix(_p(self.codes), _p(self.scales), _p(self.zeros))
+        return self._struct
 
 
 class W4Layer:
@@ -454,38 +457,48 @@ class W4Layer:
         if self.E < 1:
             raise ValueError("no routed expert")
         self.group, self.dtype, self.device = gate.group, gate.dtype, gate.device
+        self._struct = _W4Weights(gate.struct(), up.struct(), down.struct(), self.E, self.d,
+                                  self.f, self.group, _DTYPE16[self.dtype], int(self.shared))
 
     def struct(self) -> _W4Weights:
-        return _W4Weights(self.gate.struct(), self.up.struct(), self.down.struct(), self.E, self.d,
-                          self.f, self.group, _DTYPE16[self.dtype], int(self.shared))
+        return self._struct
 
 
-def _check_on(device, **tensors) -> None:
-    """Tensors (name=(tensor, shape, dtype)) on `device`, which is the current one."""
-    for name, (t, shape, dtype) in tensors.items():
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the weights on {device}")
+def _fits(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    """Raise ValueError unless t is a contiguous tensor of this shape and type on the device."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the weights on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _w4_stream(device, stream) -> int:
+    """The stream to launch on; the weights' device has to be the current one."""
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"the weights' device {device} is not the current CUDA device")
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
 
 
 def w4_gemm(x: torch.Tensor, w: W4Matrix, out: torch.Tensor | None = None, stream=None):
     """C [M, N] fp32 = x [M, K] (bf16 or fp16, the scales' type; M <= 64) times W [N, K]
     transposed, W a 4-bit matrix with group scales (moe_w4_gemm)."""
-    if w.codes.dim() != 2:
+    if not w._one:
         raise ValueError("w4_gemm takes one matrix [N, K]")
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
-    M = x.shape[0]
+    M, N, K, dev = x.shape[0], w.N, w.K, w.device
+    _fits("x", x, (M, K), w.dtype, dev)
+    s = _w4_stream(dev, stream)
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.float32, device=x.device)
-    _check_on(w.device, x=(x, (M, w.K), w.dtype), out=(out, (M, w.N), torch.float32))
-    st = w.struct()
-    _check(lib().moe_w4_gemm(_p(x), _DTYPE16[w.dtype], M, ctypes.byref(st), w.N, w.K, w.group,
-                             _p(out), _stream(stream)))
+        out = torch.empty((M, N), dtype=torch.float32, device=dev)
+    else:
+        _fits("out", out, (M, N), torch.float32, dev)
+    _check((_lib or lib()).moe_w4_gemm(x.data_ptr(), w._dtype_code, M, w._struct, N, K, w.group,
+                                       out.data_ptr(), s))
     return out
 
 
@@ -505,21 +518,27 @@ def forward_w4(x: torch.Tensor, scores: torch.Tensor, k: int, w: W4Layer,
     returns {idx, w, out}.  `outs` may hold preallocated outputs under the same names."""
     if x.dim() != 2:
         raise ValueError("x must be [T, d]")
-    T = x.shape[0]
+    T, dev = x.shape[0], w.device
+    _fits("x", x, (T, w.d), w.dtype, dev)
+    _fits("scores", scores, (T, w.E), torch.float32, dev)
+    s = _w4_stream(dev, stream)
     if ws is None:
         ws = alloc_workspace_w4(T, k, w)
-    o = dict(outs) if outs is not None else {}
-    shapes = {"idx": ((T, k), torch.int32), "w": ((T, k), torch.float32),
-              "out": ((T, w.d), torch.float32)}
-    for name, (shape, dtype) in shapes.items():
-        if name not in o:
-            o[name] = torch.empty(shape, dtype=dtype, device=x.device)
-    _check_on(w.device, x=(x, (T, w.d), w.dtype), scores=(scores, (T, w.E), torch.float32),
-              ws=(ws, ws.shape, torch.uint8), **{n: (o[n], *shapes[n]) for n in shapes})
-    st = w.struct()
-    _check(lib().moe_forward_w4(_p(scores), _p(x), T, k, ctypes.byref(st), _p(o["idx"]),
-                                _p(o["w"]), _p(o["out"]), _p(ws), ws.numel(), _stream(stream)))
-    return dict(idx=o["idx"], w=o["w"], out=o["out"])
+    elif ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous uint8 on {dev}")
+    o = {}
+    for name, shape, dtype in (("idx", (T, k), torch.int32), ("w", (T, k), torch.float32),
+                               ("out", (T, w.d), torch.float32)):
+        t = outs.get(name) if outs is not None else None
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _fits(name, t, shape, dtype, dev)
+        o[name] = t
+    _check((_lib or lib()).moe_forward_w4(scores.data_ptr(), x.data_ptr(), T, k, w._struct,
+                                          o["idx"].data_ptr(), o["w"].data_ptr(),
+                                          o["out"].data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return o
 
 
 def set_wait_limit_ns(n: int) -> None:

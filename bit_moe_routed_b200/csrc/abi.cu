@@ -996,6 +996,8 @@ int moe_w4_gemm(const void* x, int dtype, int M, const moe_w4_matrix_t* w, int N
   a.K = K;
   a.group = group;
   a.f16 = dtype == MOE_F16;
+  a.wait_ns = g_wait_ns.load();
+  a.status = di.status;
   cudaError_t e = launch_w4_gemm(a, static_cast<cudaStream_t>(stream), di.sms);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "w4_gemm launch");
 }
@@ -1061,6 +1063,8 @@ int moe_forward_w4(const float* scores, const void* x, int T, int k, const moe_w
   a.group = w->group;
   a.shared = w->shared;
   a.f16 = w->dtype == MOE_F16;
+  a.wait_ns = g_wait_ns.load();
+  a.status = di.status;
   cudaError_t e = launch_w4_layer(a, static_cast<cudaStream_t>(stream), di.sms);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "4-bit layer launch");
 }

@@ -271,6 +271,8 @@ struct W4GemmLaunch {
   float* C;           // [M][N]
   int M, N, K, group;
   bool f16;
+  long long wait_ns;
+  int* status;
 };
 cudaError_t launch_w4_gemm(const W4GemmLaunch& a, cudaStream_t s, int num_sms);
 struct W4LayerLaunch {
@@ -284,9 +286,11 @@ struct W4LayerLaunch {
   uint8_t* ws;
   int T, k, E, d, f, group, shared;
   bool f16;
+  long long wait_ns;
+  int* status;
 };
 struct W4LayerLayout {
-  size_t hh, hl, y, cnt, total;
+  size_t h, y, cnt, total;
 };
 W4LayerLayout w4_layer_layout(int T, int k, int shared, int d, int f);
 cudaError_t launch_w4_layer(const W4LayerLaunch& a, cudaStream_t s, int num_sms);

@@ -2,11 +2,9 @@
 // layers of a decode step (ai-muninn.com post, "一張 22G 老卡跑 284B": decode is bound by
 // reading the weights, so the weights are what gets small).
 //
-// One block a SM takes a contiguous range of items (16 rows of W times 8 or 16 rows of x); all
-// of its warps share an item's reduction, so even a matrix of a few thousand rows has every
-// SM reading.  More than 8 rows of x take two B sets per decoded word (64 registers instead
-// of 32), which halves how often the codes are decoded and fetched from L2; the decode, not
-// the MMAs, is what bounds a large batch.
+// One block a SM takes a contiguous range of items (16 rows of W times up to 4 rows of x); all of its warps share an item's reduction, so even a matrix of a few thousand rows has
+// every SM reading.  More than 4 rows of x are several slots of 4, each decoding the codes
+// again (they come from L2 by then).
 #include "w4.cuh"
 
 namespace bitmoe {
@@ -19,80 +17,82 @@ struct W4GemmParams {
   int M, slots;
 };
 
-template <int NB>
 struct GemmJob {
   const W4GemmParams& p;
+  __device__ __forceinline__ void range(int part, int& lo, int& hi) const {
+    const unsigned total = (unsigned)(p.slots * p.st.upe);  // below 2^23: 32 bits hold the products
+    lo = part == 0 ? (int)(blockIdx.x * total / gridDim.x) : 0;
+    hi = part == 0 ? (int)((blockIdx.x + 1) * total / gridDim.x) : 0;
+  }
   __device__ __forceinline__ int matrix(int) const { return 0; }
-  __device__ __forceinline__ void ready() const {}
-  __device__ __forceinline__ const uint16_t* row(int set, int slot, int col) const {
-    const int m = (slot * NB + set) * kW4Cols + col;
+  template <typename Wait>
+  __device__ __forceinline__ bool plan(Wait) const { return true; }
+  __device__ __forceinline__ bool same_rows() const { return false; }
+  __device__ __forceinline__ int rows(int slot) const { return min(kW4Cols, p.M - slot * kW4Cols); }
+  __device__ __forceinline__ const uint16_t* row(int slot, int col) const {
+    const int m = slot * kW4Cols + col;
     return m < p.M ? p.x + (size_t)m * p.st.K : nullptr;
   }
   __device__ __forceinline__ void store(int slot, int unit, int col, int r, float a, float b) const {
-    const int m = slot * NB * kW4Cols + col, n = unit * kW4Rows + r;
+    const int m = slot * kW4Cols + col, n = unit * kW4Rows + r;
     if (m >= p.M) return;
     float* c = p.C + (size_t)m * p.st.rows + n;
     if (n < p.st.rows) c[0] = a;
     if (n + 8 < p.st.rows) c[8] = b;
   }
-  __device__ __forceinline__ void batch_done(int, int, int) const {}
+  __device__ __forceinline__ void before_add(int) const {}
+  __device__ __forceinline__ void finish(int) const {}
 };
 
-template <typename T, int G, bool ZP, int NB>
-__global__ void __launch_bounds__(kW4MaxWarps * 32, 1) w4_gemm_kernel(const __grid_constant__ W4GemmParams p) {
-  extern __shared__ __align__(128) uint8_t w4_smem[];
-  const long long total = (long long)p.slots * p.st.upe;
-  const int lo = (int)(blockIdx.x * total / gridDim.x), hi = (int)((blockIdx.x + 1) * total / gridDim.x);
-  GemmJob<NB> job{p};
-  w4_stream<T, T, G, ZP, NB, false, false>(p.st, w4_smem, lo, hi, job);
+template <typename T, int G, bool ZP, bool RING>
+__global__ void __launch_bounds__(kW4MaxThreads, 1) w4_gemm_kernel(const __grid_constant__ W4GemmParams p) {
+  extern __shared__ uint8_t w4_raw[];
+  uint8_t* smem = w4_raw + ((1024 - (ptx::smem_u32(w4_raw) & 1023)) & 1023);
+  w4_init(p.st, smem, w4_smem<G, ZP, RING>(p.st));
+  __syncthreads();
+  GemmJob job{p};
+  if (w4_roles<T, T, G, ZP, RING, false>(p.st, smem, job)) w4_consume<T, T, G, ZP, RING, false>(p.st, smem, job);
 }
 
-template <typename T, int G, bool ZP, int NB>
+template <typename T, int G, bool ZP, bool RING>
 cudaError_t launch_one(const W4GemmParams& p, int blocks, int warps, cudaStream_t s) {
-  auto kern = w4_gemm_kernel<T, G, ZP, NB>;
-  const size_t smem = w4_stream_smem(warps);
+  auto kern = w4_gemm_kernel<T, G, ZP, RING>;
+  const size_t smem = (size_t)w4_smem<G, ZP, RING>(p.st).bytes() + kW4SmemPad;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)warps * 32), smem, s, false, p);
-}
-template <typename T, int G, bool ZP>
-cudaError_t launch_nb(const W4GemmParams& p, int nb, int blocks, int warps, cudaStream_t s) {
-  return nb == 1 ? launch_one<T, G, ZP, 1>(p, blocks, warps, s) : launch_one<T, G, ZP, 2>(p, blocks, warps, s);
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)w4_threads(warps)), smem, s, false, p);
 }
 template <typename T, int G>
-cudaError_t launch_z(const W4GemmParams& p, int nb, int blocks, int warps, cudaStream_t s) {
-  return p.st.m0.zeros ? launch_nb<T, G, true>(p, nb, blocks, warps, s)
-                       : launch_nb<T, G, false>(p, nb, blocks, warps, s);
+cudaError_t launch_z(const W4GemmParams& p, int blocks, int warps, cudaStream_t s) {
+  if (p.st.zeros0)
+    return p.st.ring_scales ? launch_one<T, G, true, true>(p, blocks, warps, s)
+                            : launch_one<T, G, true, false>(p, blocks, warps, s);
+  return p.st.ring_scales ? launch_one<T, G, false, true>(p, blocks, warps, s)
+                          : launch_one<T, G, false, false>(p, blocks, warps, s);
 }
 template <typename T>
-cudaError_t launch_g(const W4GemmParams& p, int group, int nb, int blocks, int warps, cudaStream_t s) {
-  if (group == 32) return launch_z<T, 32>(p, nb, blocks, warps, s);
-  if (group == 64) return launch_z<T, 64>(p, nb, blocks, warps, s);
-  return launch_z<T, 128>(p, nb, blocks, warps, s);
+cudaError_t launch_g(const W4GemmParams& p, int group, int blocks, int warps, cudaStream_t s) {
+  if (group == 32) return launch_z<T, 32>(p, blocks, warps, s);
+  if (group == 64) return launch_z<T, 64>(p, blocks, warps, s);
+  return launch_z<T, 128>(p, blocks, warps, s);
 }
 
 }  // namespace
 
 cudaError_t launch_w4_gemm(const W4GemmLaunch& a, cudaStream_t s, int num_sms) {
   W4GemmParams p{};
-  const W4Split sp = w4_split(a.K);
-  p.st.m0 = {a.codes, a.scales, a.zeros};
-  p.st.K = a.K;
-  p.st.rows = a.N;
-  p.st.upe = (a.N + kW4Rows - 1) / kW4Rows;
-  p.st.passes = sp.passes;
-  p.st.kw = sp.kw;
-  p.st.teams = sp.teams;
-  p.st.vec = w4_vec(a.scales, a.zeros, a.K, a.group);
+  if (!w4_set_stream(p.st, {a.codes, a.scales, a.zeros}, nullptr, 1, a.N, a.K, a.group))
+    return cudaErrorInvalidValue;
+  p.st.wait_ns = a.wait_ns;
+  p.st.status = a.status;
   p.x = a.x;
   p.C = a.C;
   p.M = a.M;
-  const int nb = a.M > kW4Cols ? 2 : 1;
-  p.slots = (a.M + nb * kW4Cols - 1) / (nb * kW4Cols);
+  p.slots = (a.M + kW4Cols - 1) / kW4Cols;
   const long long total = (long long)p.slots * p.st.upe;
+  const int warps = p.st.kw * p.st.teams;
   const int blocks = (int)(total < num_sms ? total : num_sms);
-  return a.f16 ? launch_g<FP16>(p, a.group, nb, blocks, sp.warps(), s)
-               : launch_g<BF16>(p, a.group, nb, blocks, sp.warps(), s);
+  return a.f16 ? launch_g<FP16>(p, a.group, blocks, warps, s) : launch_g<BF16>(p, a.group, blocks, warps, s);
 }
 
 }  // namespace bitmoe

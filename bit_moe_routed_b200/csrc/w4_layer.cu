@@ -7,19 +7,20 @@
 // dpshk.com article, "核心实现三": an expert is read once for all its tokens).
 //
 //   kernel 1  routing, grouping by expert, gate and up products, silu(g) u
-//   kernel 2  routing and grouping again, down product, weighted sum
+//   kernel 2  routing and grouping again, down product, weighted sum (up to 8 tokens; with
+//             more a third, small one adds up)
 //
-// Both are w4_stream loops over (slot, unit) items, a slot being an expert with up to 8 of
-// its (token, choice) pairs, the shared expert's slots first, then the experts in ascending
+// Both are w4_stream loops over (slot, unit) items, a slot being an expert with up to 4 of its
+// (token, choice) pairs, the shared expert's slots first, then the experts in ascending
 // order.  What bounds them is reading the active experts' codes once.  Every block works out
 // the routing and the slots for itself from the scores (one warp a token): that costs about
 // a microsecond in shared memory, where a kernel of its own would cost a launch and a round
 // trip through L2, and it lets kernel 2 start its weight copies before kernel 1 has
 // finished.  The blocks' slots agree because pairs are ranked in (token, choice) order.
-// h goes to kernel 2 as two bf16 terms, high and low: 16 significant bits, so that the fp32
-// output keeps about 6e-7 of relative error, at one more MMA per fragment, which the loop
-// has room for; bf16 alone would leave 1.7e-3.  Its terms cannot overflow where fp16's could.
-// The weighted sum runs where the last slot of 16 output rows finishes (an acq_rel count, as
+// h stays fp32 in the workspace and enters the down product as x does the first two, as
+// 31-bit fixed point per 256 elements; in 16 bits it would leave 1.7e-3 (bf16) of relative
+// error in an fp32 output.
+// The weighted sum of a few tokens runs where the last slot of 16 output rows finishes (an acq_rel count, as
 // in the single-token kernel), always in the order shared, j = 0..k-1.
 #include "single_token.cuh"
 #include "w4.cuh"
@@ -33,7 +34,7 @@ struct W4LayerParams {
   int T, E, k, P, shared;  // P = T * k pairs; row P + t is token t's shared-expert row
   int slots_cap;
   const uint16_t* x;       // kernel 1
-  uint16_t *hh, *hl;       // h, high and low bf16 terms [rows][f]
+  float* h;                // [rows][f]
   int32_t* idx;
   float* w_out;
   float* y;                // [rows][d] fp32
@@ -43,21 +44,33 @@ struct W4LayerParams {
   int f, d;
 };
 
-// The slots in shared memory: 8 pairs, the expert and the count of each; the pairs' weights.
+// The slots in shared memory: up to kW4Cols pairs, the expert and the count of each; the
+// pairs' weights.  The shared expert's slots, the first, are known without them: slot s has
+// tokens s kW4Cols and up.
 struct W4Plan {
-  uint16_t* pair;  // [slots][8]
+  uint16_t* pair;  // [slots][kW4Cols]
   int16_t* e;
-  int16_t* n;
+  uint8_t* n;
   float* w;        // [P]
-  int slots;
+  int* total;      // slots
 };
-__host__ __device__ inline int w4_slots_cap(int T, int k, int E, int shared) {
+inline int w4_slots_cap(int T, int k, int E, int shared) {
+  constexpr int sc = kW4Cols;
   const int P = T * k;
-  const int routed = P < E + P / kW4Cols ? P : E + P / kW4Cols;
-  return routed + (shared ? (T + kW4Cols - 1) / kW4Cols : 0);
+  const int routed = P < E + P / sc ? P : E + P / sc;
+  return routed + (shared ? (T + sc - 1) / sc : 0);
 }
 inline size_t w4_plan_smem(int T, int k, int E, int shared) {
-  return (size_t)w4_slots_cap(T, k, E, shared) * 20 + (size_t)T * k * 4 + 16 + 4 * kW4Batch * kW4MaxWarps;
+  return (size_t)w4_slots_cap(T, k, E, shared) * (2 * kW4Cols + 3) + (size_t)T * k * 4 + 16 + 16;
+}
+__device__ __forceinline__ W4Plan w4_plan_at(const W4LayerParams& p, uint8_t* at) {
+  W4Plan L;
+  L.total = reinterpret_cast<int*>(at);
+  L.w = reinterpret_cast<float*>(at + 16);
+  L.pair = reinterpret_cast<uint16_t*>(at + 16 + (((size_t)p.P * 4 + 15) & ~(size_t)15));
+  L.e = reinterpret_cast<int16_t*>(L.pair + (size_t)p.slots_cap * kW4Cols);
+  L.n = reinterpret_cast<uint8_t*>(L.e + p.slots_cap);
+  return L;
 }
 
 __device__ __forceinline__ void w4_route(const float* scores, int E, int k, int lane, int* slot_e,
@@ -70,32 +83,31 @@ __device__ __forceinline__ void w4_route(const float* scores, int E, int k, int 
     route_token_warp<32>(scores, E, k, lane, slot_e, nullptr, nullptr, w, pos, nullptr, nullptr, nullptr, nullptr);
 }
 
-// Routing and slots.  scratch: shared memory that the stream uses later (at least
-// 8 P + 8 E + 256 bytes a warp).  With `emit` the block writes idx and w.
-__device__ __forceinline__ W4Plan w4_plan(const W4LayerParams& p, uint8_t* at, uint8_t* scratch,
-                                          bool emit) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  W4Plan L;
-  L.w = reinterpret_cast<float*>(at);
-  L.pair = reinterpret_cast<uint16_t*>(at + (((size_t)p.P * 4 + 15) & ~(size_t)15));
-  L.e = reinterpret_cast<int16_t*>(L.pair + (size_t)p.slots_cap * 8);
-  L.n = L.e + p.slots_cap;
-  int* se = reinterpret_cast<int*>(scratch);  // expert of a pair
-  int* rank = se + p.P;                       // its place among the expert's pairs
-  int* cnt = rank + p.P;                      // pairs, then first slot, of an expert
-  int* base = cnt + p.E;
-  int* tmp = base + p.E + warp * 64;
+// Routing and slots, by the consuming warps, which then let the copying warp at them.
+// scratch: the memory of the stream's sums (2 KB a warp; it takes 4 P + 4 E + 256 bytes a warp,
+// at most 14.6 KB of the 18 KB of the fewest warps, 9, with 64 tokens, k = 32, E = 1024).  With
+// `emit` the block writes idx and w.
+__device__ __forceinline__ void w4_plan(const W4LayerParams& p, const W4Plan& L, uint8_t* scratch, uint32_t ready,
+                                        bool emit) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = p.st.kw * p.st.teams, threads = warps * 32;
+  int* tmp = reinterpret_cast<int*>(scratch) + warp * 64;
+  int* sum = reinterpret_cast<int*>(scratch);  // a warp's slots (after the routing)
+  uint16_t* se = reinterpret_cast<uint16_t*>(scratch + warps * 256);  // expert of a pair
+  uint16_t* rank = se + p.P;                   // its place among the expert's pairs
+  uint16_t* cnt = rank + p.P;                  // pairs of an expert
+  uint16_t* base = cnt + p.E;                  // its first slot
   const int ss = p.shared ? (p.T + kW4Cols - 1) / kW4Cols : 0;
-  for (int i = threadIdx.x; i < p.E; i += blockDim.x) cnt[i] = 0;
+  for (int i = threadIdx.x; i < p.E; i += threads) cnt[i] = 0;
   for (int t = warp; t < p.T; t += warps) {
     w4_route(p.scores + (size_t)t * p.E, p.E, p.k, lane, tmp, L.w + t * p.k, tmp + 32);
     __syncwarp();
-    if (lane < p.k) se[t * p.k + lane] = tmp[tmp[32 + lane]];
+    if (lane < p.k) se[t * p.k + lane] = (uint16_t)tmp[tmp[32 + lane]];
     __syncwarp();
   }
-  __syncthreads();
+  w4_sync(p.st);
   if (emit)
-    for (int i = threadIdx.x; i < p.P; i += blockDim.x) {
+    for (int i = threadIdx.x; i < p.P; i += threads) {
       p.idx[i] = se[i];
       p.w_out[i] = L.w[i];
     }
@@ -109,49 +121,125 @@ __device__ __forceinline__ W4Plan w4_plan(const W4LayerParams& p, uint8_t* at, u
       int c = 0;
       if (i < p.P) {
         c = cnt[e];
-        rank[i] = c + before;
+        rank[i] = (uint16_t)(c + before);
       }
       __syncwarp();
-      if (i < p.P && before == 0) cnt[e] = c + __popc(same);
+      if (i < p.P && before == 0) cnt[e] = (uint16_t)(c + __popc(same));
       __syncwarp();
     }
-    int run = ss;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < p.E ? (cnt[e] + kW4Cols - 1) / kW4Cols : 0;
-      int inc = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-      }
-      if (e < p.E) base[e] = run + inc - n;
-      run += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) tmp[0] = run;
   }
-  __syncthreads();
-  L.slots = *(base + p.E);  // warp 0's tmp[0]
-  for (int i = threadIdx.x; i < p.P; i += blockDim.x) {
-    const int e = se[i], r = rank[i], s = base[e] + r / kW4Cols;
-    L.pair[s * 8 + r % kW4Cols] = (uint16_t)i;
+  w4_sync(p.st);
+  // first slots: each warp takes a run of experts, 32 at a time
+  const int per = (p.E + 32 * warps - 1) / (32 * warps) * 32;
+  int run = 0;
+  for (int e0 = warp * per; e0 < min(p.E, (warp + 1) * per); e0 += 32) {
+    const int e = e0 + lane;
+    const int n = e < p.E ? (cnt[e] + kW4Cols - 1) / kW4Cols : 0;
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (e < p.E) base[e] = (uint16_t)(run + inc - n);
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) sum[warp] = run;
+  w4_sync(p.st);
+  for (int i = threadIdx.x; i < p.P; i += threads) {
+    const int e = se[i], r = rank[i];
+    int s = ss + base[e] + r / kW4Cols;
+    for (int w = 0; w < e / per; ++w) s += sum[w];
+    L.pair[s * kW4Cols + r % kW4Cols] = (uint16_t)i;
     if (r % kW4Cols == 0) {
       L.e[s] = (int16_t)e;
-      L.n[s] = (int16_t)min(kW4Cols, cnt[e] - r);
+      L.n[s] = (uint8_t)min(kW4Cols, cnt[e] - r);
     }
   }
-  if (p.shared)
-    for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
-      const int s = t / kW4Cols;
-      L.pair[t] = (uint16_t)(p.P + t);
-      if (t % kW4Cols == 0) {
-        L.e[s] = (int16_t)p.E;
-        L.n[s] = (int16_t)min(kW4Cols, p.T - t);
+  if (threadIdx.x == 0) {
+    int s = ss;
+    for (int w = 0; w < warps; ++w) s += sum[w];
+    *L.total = s;
+  }
+  w4_sync(p.st);  // the scratch is the stream's from here on
+  // the copying and adding warps may read the slots
+  if (threadIdx.x == 0) ptx::mbar_arrive(ready);
+}
+
+// The same for up to 4 tokens with up to 32 pairs, by the adding warps, while the consuming ones
+// begin with the shared expert: no expert has more pairs than a slot takes, so a slot is an
+// expert, in the order in which the pairs name them.  scratch: 256 bytes a warp and 32 ints.
+__host__ __device__ inline bool w4_few(int T, int k) { return T <= kW4Cols && T * k <= 32; }
+__device__ __forceinline__ void w4_plan_few(const W4LayerParams& p, const W4Plan& L, uint8_t* scratch,
+                                            uint32_t ready, int tid, bool emit) {
+  const int warp = tid >> 5, lane = tid & 31, ss = p.shared ? 1 : 0;
+  int* se = reinterpret_cast<int*>(scratch);
+  int* tmp = se + 32 + warp * 64;
+  for (int t = warp; t < p.T; t += kW4SumThreads / 32) {
+    w4_route(p.scores + (size_t)t * p.E, p.E, p.k, lane, tmp, L.w + t * p.k, tmp + 32);
+    __syncwarp();
+    if (lane < p.k) se[t * p.k + lane] = tmp[tmp[32 + lane]];
+    __syncwarp();
+  }
+  asm volatile("bar.sync 3, %0;" ::"n"(kW4SumThreads) : "memory");
+  if (warp == 0) {
+    const int e = lane < p.P ? se[lane] : -1 - lane;
+    const unsigned same = __match_any_sync(0xffffffffu, e), lower = (1u << lane) - 1u;
+    const bool first = lane < p.P && (same & lower) == 0;
+    const unsigned firsts = __ballot_sync(0xffffffffu, first);
+    const int s = ss + __popc(firsts & ((1u << (__ffs(same) - 1)) - 1u));
+    if (lane < p.P) {
+      L.pair[s * kW4Cols + __popc(same & lower)] = (uint16_t)lane;
+      if (first) {
+        L.e[s] = (int16_t)e;
+        L.n[s] = (uint8_t)__popc(same);
+      }
+      if (emit) {
+        p.idx[lane] = e;
+        p.w_out[lane] = L.w[lane];
       }
     }
-  __syncthreads();  // the scratch is the stream's from here on
-  return L;
+    if (lane == 0) *L.total = ss + __popc(firsts);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ready);
+  }
 }
+
+// What both kernels' jobs share: the slots, and the block's items: its share of the shared
+// expert's (which the copying warp can start on before the routing is known) and the rest.
+struct LayerJob {
+  const W4LayerParams& p;
+  W4Plan L;
+  uint8_t* scratch;  // for w4_plan_few
+  uint32_t ready;    // barrier: the slots are known
+  __device__ __forceinline__ int shared_slots() const { return p.shared ? (p.T + kW4Cols - 1) / kW4Cols : 0; }
+  __device__ __forceinline__ void range(int part, int& lo, int& hi) const {
+    // at most 2^22 items: 32 bits hold the products
+    const unsigned S = (unsigned)(shared_slots() * p.st.upe), G = gridDim.x, b = blockIdx.x;
+    const unsigned s0 = b * S / G, s1 = (b + 1) * S / G;
+    lo = (int)s0;
+    hi = (int)s1;
+    if (part == 0) return;
+    const unsigned all = (unsigned)(*L.total * p.st.upe);
+    if (all - S >= G) {  // whole shares of everything, less the block's shared items
+      lo = (int)(S + b * all / G - s0);
+      hi = (int)(S + (b + 1) * all / G - s1);
+    } else {
+      lo = (int)(S + b * (all - S) / G);
+      hi = (int)(S + (b + 1) * (all - S) / G);
+    }
+  }
+  __device__ __forceinline__ int matrix(int slot) const { return slot < shared_slots() ? p.E : L.e[slot]; }
+  template <typename Wait>
+  __device__ __forceinline__ bool plan(Wait wait) const { return wait(); }
+  __device__ __forceinline__ int rows(int slot) const {
+    return slot < shared_slots() ? min(kW4Cols, p.T - slot * kW4Cols) : L.n[slot];
+  }
+  // the y row (and row of h) of a column
+  __device__ __forceinline__ int pair(int slot, int col) const {
+    return slot < shared_slots() ? p.P + slot * kW4Cols + col : L.pair[slot * kW4Cols + col];
+  }
+};
 
 __device__ __forceinline__ int w4_atom_add_acq_rel(int* p, int v) {
   int old;
@@ -160,125 +248,160 @@ __device__ __forceinline__ int w4_atom_add_acq_rel(int* p, int v) {
   return old;
 }
 
-struct GateUpJob {
-  const W4LayerParams& p;
-  const W4Plan& L;
-  __device__ __forceinline__ int matrix(int slot) const { return L.e[slot]; }
-  __device__ __forceinline__ void ready() const {}
-  __device__ __forceinline__ const uint16_t* row(int, int slot, int col) const {
-    if (col >= L.n[slot]) return nullptr;
-    const int pr = L.pair[slot * 8 + col];
-    const int tok = pr < p.P ? pr / p.k : pr - p.P;
-    return p.x + (size_t)tok * p.d;
+struct GateUpJob : LayerJob {
+  __device__ __forceinline__ const uint16_t* row(int slot, int col) const {
+    if (col >= rows(slot)) return nullptr;
+    const int pr = pair(slot, col);
+    return p.x + (size_t)(pr < p.P ? pr / p.k : pr - p.P) * p.d;
   }
   __device__ __forceinline__ void store(int slot, int unit, int col, int r, float g, float u) const {
-    if (col >= L.n[slot]) return;
-    const float h = g / (1.0f + expf(-g)) * u;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-    const float hf = __bfloat162float(hi);
-    // an infinite or NaN h has no low term
-    const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(hf) <= 3.4e38f ? h - hf : 0.f);
-    const size_t at = (size_t)L.pair[slot * 8 + col] * p.f + unit * 8 + r;
-    p.hh[at] = __bfloat16_as_ushort(hi);
-    p.hl[at] = __bfloat16_as_ushort(lo);
+    p.h[(size_t)pair(slot, col) * p.f + unit * 8 + r] = g / (1.0f + expf(-g)) * u;
   }
-  __device__ __forceinline__ void batch_done(int, int, int) const {}
+  __device__ __forceinline__ bool same_rows() const { return p.T == 1; }
+  __device__ __forceinline__ void before_add(int tid) const {
+    if (w4_few(p.T, p.k)) w4_plan_few(p, L, scratch, ready, tid, blockIdx.x == 0);
+  }
+  __device__ __forceinline__ void finish(int) const {}
 };
 
-struct DownJob {
-  const W4LayerParams& p;
-  const W4Plan& L;
-  int* last;
-  __device__ __forceinline__ int matrix(int slot) const { return L.e[slot]; }
-  __device__ __forceinline__ void ready() const { ptx::griddep_wait(); }  // h and the counts
-  __device__ __forceinline__ const uint16_t* row(int set, int slot, int col) const {
-    if (col >= L.n[slot]) return nullptr;
-    return (set ? p.hl : p.hh) + (size_t)L.pair[slot * 8 + col] * p.f;
+// The weighted sum of four outputs of token t.
+__device__ __forceinline__ void w4_sum4(const W4LayerParams& p, const float* w, int t, int m) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.shared) a = __ldcg(reinterpret_cast<const float4*>(p.y + (size_t)(p.P + t) * p.d + m));
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < p.k)
+        v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + (size_t)(t * p.k + j0 + j) * p.d + m));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < p.k) {
+        const float c = w[j0 + j];
+        a.x = fmaf(c, v[j].x, a.x);
+        a.y = fmaf(c, v[j].y, a.y);
+        a.z = fmaf(c, v[j].z, a.z);
+        a.w = fmaf(c, v[j].w, a.w);
+      }
+  }
+  *reinterpret_cast<float4*>(p.out + (size_t)t * p.d + m) = a;
+}
+
+// Up to kW4InlineT tokens the block that finishes a unit's last slot adds the unit's rows up,
+// all of its threads together, after its last store.  With more tokens the last blocks would
+// have most of the sum to themselves; there a third kernel does it.
+constexpr int kW4InlineT = 8;
+struct DownJob : LayerJob {
+  int* list;   // [units2], in memory that the stream has finished with
+  int* count;  // 0 at the start
+  __device__ __forceinline__ const float* row(int slot, int col) const {
+    return col < rows(slot) ? p.h + (size_t)pair(slot, col) * p.f : nullptr;
   }
   __device__ __forceinline__ void store(int slot, int unit, int col, int r, float a, float b) const {
-    if (col >= L.n[slot]) return;
-    float* y = p.y + (size_t)L.pair[slot * 8 + col] * p.d + unit * kW4Rows + r;
+    float* y = p.y + (size_t)pair(slot, col) * p.d + unit * kW4Rows + r;
     y[0] = a;
     y[8] = b;
   }
-  __device__ __forceinline__ void batch_done(int, int u0, int nb) const {
-    __syncthreads();
-    if (threadIdx.x < nb)
-      last[threadIdx.x] = w4_atom_add_acq_rel(p.cnt + u0 + threadIdx.x, 1) == L.slots - 1;
-    __syncthreads();
-    for (int q = 0; q < nb; ++q) {
-      if (!last[q]) continue;
-      for (int i = threadIdx.x; i < p.T * 4; i += blockDim.x) {
-        const int t = i >> 2, m = (u0 + q) * kW4Rows + 4 * (i & 3);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.shared) a = __ldcg(reinterpret_cast<const float4*>(p.y + (size_t)(p.P + t) * p.d + m));
-        for (int j = 0; j < p.k; ++j) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.y + (size_t)(t * p.k + j) * p.d + m));
-          const float w = L.w[t * p.k + j];
-          a.x = fmaf(w, v.x, a.x);
-          a.y = fmaf(w, v.y, a.y);
-          a.z = fmaf(w, v.z, a.z);
-          a.w = fmaf(w, v.w, a.w);
-        }
-        *reinterpret_cast<float4*>(p.out + (size_t)t * p.d + m) = a;
+  __device__ __forceinline__ bool same_rows() const { return false; }
+  __device__ __forceinline__ void before_add(int tid) const {
+    if (w4_few(p.T, p.k)) w4_plan_few(p, L, scratch, ready, tid, false);
+    ptx::griddep_wait();
+  }
+  // by all consuming and adding threads
+  __device__ __forceinline__ void finish(int tid) const {
+    if (p.T > kW4InlineT) return;
+    const int threads = p.st.kw * p.st.teams * 32 + kW4SumThreads;
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");  // every store
+    for (int part = 0; part < 2; ++part) {
+      int lo, hi;
+      range(part, lo, hi);
+      for (int i = lo + tid; i < hi; i += threads) {
+        const int u = i % p.st.upe;
+        if (w4_atom_add_acq_rel(p.cnt + u, 1) == *L.total - 1) list[atomicAdd(count, 1)] = u;
       }
+    }
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    const int work = *count * p.T * 4;
+    for (int i = tid; i < work; i += threads) {
+      const int t = (i >> 2) % p.T;
+      w4_sum4(p, L.w + t * p.k, t, list[(i >> 2) / p.T] * kW4Rows + 4 * (i & 3));
     }
   }
 };
 
-template <typename T, int G, bool ZP>
-__global__ void __launch_bounds__(kW4MaxWarps * 32, 1) w4_gate_up_kernel(const __grid_constant__ W4LayerParams p) {
-  extern __shared__ __align__(128) uint8_t w4_smem[];
+__global__ void __launch_bounds__(256) w4_sum_kernel(const __grid_constant__ W4LayerParams p) {
+  ptx::griddep_wait();
+  const int i = blockIdx.x * 256 + threadIdx.x, per = p.d / 4;
+  if (i < p.T * per) w4_sum4(p, p.w_out + i / per * p.k, i / per, i % per * 4);
+}
+
+template <typename T, int G, bool ZP, bool RING>
+__global__ void __launch_bounds__(kW4MaxThreads, 1) w4_gate_up_kernel(const __grid_constant__ W4LayerParams p) {
+  extern __shared__ uint8_t w4_raw[];
+  uint8_t* smem = w4_raw + ((1024 - (ptx::smem_u32(w4_raw) & 1023)) & 1023);
   ptx::griddep_launch_dependents();
-  uint8_t* at = w4_smem + (size_t)(blockDim.x >> 5) * (kW4Stages * kW4StageBytes + 2 * kW4Batch * 512);
-  const W4Plan L = w4_plan(p, at, w4_smem, blockIdx.x == 0);
+  const W4Smem M = w4_smem<G, ZP, RING>(p.st);
+  w4_init(p.st, smem, M);
+  const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * (2 * kW4MaxRing + 4);
+  GateUpJob job{{p, w4_plan_at(p, smem + M.bytes()), smem + M.few(), ready}};
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.units2; i += blockDim.x) p.cnt[i] = 0;
-  const long long total = (long long)L.slots * p.st.upe;
-  const int lo = (int)(blockIdx.x * total / gridDim.x), hi = (int)((blockIdx.x + 1) * total / gridDim.x);
-  GateUpJob job{p, L};
-  w4_stream<T, T, G, ZP, 1, false, true>(p.st, w4_smem, lo, hi, job);
+  __syncthreads();
+  if (!w4_roles<T, T, G, ZP, RING, true>(p.st, smem, job)) return;
+  if (!w4_few(p.T, p.k)) w4_plan(p, job.L, smem + M.part(), ready, blockIdx.x == 0);
+  w4_consume<T, T, G, ZP, RING, true>(p.st, smem, job);
 }
 
-template <typename S, int G, bool ZP>
-__global__ void __launch_bounds__(kW4MaxWarps * 32, 1) w4_down_kernel(const __grid_constant__ W4LayerParams p) {
-  extern __shared__ __align__(128) uint8_t w4_smem[];
-  uint8_t* at = w4_smem + (size_t)(blockDim.x >> 5) * (kW4Stages * kW4StageBytes + 2 * kW4Batch * 512);
-  int* last = reinterpret_cast<int*>(at);
-  const W4Plan L = w4_plan(p, at + 4 * kW4Batch * kW4MaxWarps, w4_smem, false);
-  const long long total = (long long)L.slots * p.st.upe;
-  const int lo = (int)(blockIdx.x * total / gridDim.x), hi = (int)((blockIdx.x + 1) * total / gridDim.x);
-  DownJob job{p, L, last};
-  w4_stream<BF16, S, G, ZP, 2, true, false>(p.st, w4_smem, lo, hi, job);
+template <typename S, int G, bool ZP, bool RING>
+__global__ void __launch_bounds__(kW4MaxThreads, 1) w4_down_kernel(const __grid_constant__ W4LayerParams p) {
+  extern __shared__ uint8_t w4_raw[];
+  uint8_t* smem = w4_raw + ((1024 - (ptx::smem_u32(w4_raw) & 1023)) & 1023);
+  ptx::griddep_launch_dependents();
+  const W4Smem M = w4_smem<G, ZP, RING>(p.st);
+  w4_init(p.st, smem, M);
+  const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * (2 * kW4MaxRing + 4);
+  DownJob job{{p, w4_plan_at(p, smem + M.bytes()), smem + M.few(), ready},
+                               reinterpret_cast<int*>(smem), reinterpret_cast<int*>(smem + M.counter())};
+  __syncthreads();
+  if (!w4_roles<FP32, S, G, ZP, RING, false>(p.st, smem, job)) return;
+  if (!w4_few(p.T, p.k)) w4_plan(p, job.L, smem + M.part(), ready, false);
+  ptx::griddep_wait();  // h and the counts
+  w4_consume<FP32, S, G, ZP, RING, false>(p.st, smem, job);
+  job.finish(threadIdx.x);
 }
 
+template <typename T, int G, bool ZP, bool RING>
+cudaError_t launch_gate_up(const W4LayerParams& p, int blocks, cudaStream_t s) {
+  auto kern = w4_gate_up_kernel<T, G, ZP, RING>;
+  const size_t smem = w4_smem<G, ZP, RING>(p.st).bytes() + w4_plan_smem(p.T, p.k, p.E, p.shared) + kW4SmemPad;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)w4_threads(p.st.kw * p.st.teams)), smem, s, false, p);
+}
+template <typename S, int G, bool ZP, bool RING>
+cudaError_t launch_down(const W4LayerParams& p, int blocks, cudaStream_t s) {
+  auto kern = w4_down_kernel<S, G, ZP, RING>;
+  const size_t smem = w4_smem<G, ZP, RING>(p.st).bytes() + w4_plan_smem(p.T, p.k, p.E, p.shared) + kW4SmemPad;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)w4_threads(p.st.kw * p.st.teams)), smem, s, true, p);
+}
 template <typename T, int G, bool ZP>
-cudaError_t launch_both(const W4LayerParams& p1, const W4LayerParams& p2, int warps1, int warps2,
-                        int blocks, cudaStream_t s) {
-  auto k1 = w4_gate_up_kernel<T, G, ZP>;
-  auto k2 = w4_down_kernel<T, G, ZP>;
-  const size_t plan = w4_plan_smem(p1.T, p1.k, p1.E, p1.shared);
-  const size_t smem1 = w4_stream_smem(warps1) + plan, smem2 = w4_stream_smem(warps2) + plan;
-  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem2);
+cudaError_t launch_both(const W4LayerParams& p1, const W4LayerParams& p2, int blocks, cudaStream_t s) {
+  cudaError_t e = p1.st.ring_scales ? launch_gate_up<T, G, ZP, true>(p1, blocks, s)
+                                    : launch_gate_up<T, G, ZP, false>(p1, blocks, s);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k1, dim3((unsigned)blocks), dim3((unsigned)warps1 * 32), smem1, s, false, p1);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k2, dim3((unsigned)blocks), dim3((unsigned)warps2 * 32), smem2, s, true, p2);
-}
-template <typename T, int G>
-cudaError_t launch_z(const W4LayerParams& p1, const W4LayerParams& p2, int warps1, int warps2,
-                     int blocks, cudaStream_t s) {
-  return p1.st.m0.zeros ? launch_both<T, G, true>(p1, p2, warps1, warps2, blocks, s)
-                        : launch_both<T, G, false>(p1, p2, warps1, warps2, blocks, s);
+  e = p2.st.ring_scales ? launch_down<T, G, ZP, true>(p2, blocks, s) : launch_down<T, G, ZP, false>(p2, blocks, s);
+  if (e != cudaSuccess || p2.T <= kW4InlineT) return e;
+  const unsigned sum_blocks = (unsigned)(((long long)p2.T * (p2.d / 4) + 255) / 256);
+  return launch_pdl(w4_sum_kernel, dim3(sum_blocks), dim3(256), 0, s, true, p2);
 }
 template <typename T>
-cudaError_t launch_g(const W4LayerParams& p1, const W4LayerParams& p2, int group, int warps1,
-                     int warps2, int blocks, cudaStream_t s) {
-  if (group == 32) return launch_z<T, 32>(p1, p2, warps1, warps2, blocks, s);
-  if (group == 64) return launch_z<T, 64>(p1, p2, warps1, warps2, blocks, s);
-  return launch_z<T, 128>(p1, p2, warps1, warps2, blocks, s);
+cudaError_t launch_g(const W4LayerParams& p1, const W4LayerParams& p2, int group, int blocks, cudaStream_t s) {
+  const bool z = p1.st.zeros0 != nullptr;
+  if (group == 32) return z ? launch_both<T, 32, true>(p1, p2, blocks, s) : launch_both<T, 32, false>(p1, p2, blocks, s);
+  if (group == 64) return z ? launch_both<T, 64, true>(p1, p2, blocks, s) : launch_both<T, 64, false>(p1, p2, blocks, s);
+  return z ? launch_both<T, 128, true>(p1, p2, blocks, s) : launch_both<T, 128, false>(p1, p2, blocks, s);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -289,10 +412,8 @@ W4LayerLayout w4_layer_layout(int T, int k, int shared, int d, int f) {
   W4LayerLayout L{};
   const size_t R = (size_t)T * k + (shared ? T : 0);
   size_t o = 0;
-  L.hh = o;
-  o = up256(o + R * f * 2);
-  L.hl = o;
-  o = up256(o + R * f * 2);
+  L.h = o;
+  o = up256(o + R * f * 4);
   L.y = o;
   o = up256(o + R * d * 4);
   L.cnt = o;
@@ -310,10 +431,8 @@ cudaError_t launch_w4_layer(const W4LayerLaunch& a, cudaStream_t s, int num_sms)
   p.k = a.k;
   p.P = a.T * a.k;
   p.shared = a.shared;
-  p.slots_cap = w4_slots_cap(a.T, a.k, a.E, a.shared);
   p.x = a.x;
-  p.hh = reinterpret_cast<uint16_t*>(a.ws + L.hh);
-  p.hl = reinterpret_cast<uint16_t*>(a.ws + L.hl);
+  p.h = reinterpret_cast<float*>(a.ws + L.h);
   p.y = reinterpret_cast<float*>(a.ws + L.y);
   p.cnt = reinterpret_cast<int*>(a.ws + L.cnt);
   p.idx = a.idx;
@@ -322,28 +441,16 @@ cudaError_t launch_w4_layer(const W4LayerLaunch& a, cudaStream_t s, int num_sms)
   p.f = a.f;
   p.d = a.d;
   p.units2 = a.d / kW4Rows;
+  p.st.wait_ns = a.wait_ns;
+  p.st.status = a.status;
   W4LayerParams p1 = p, p2 = p;
-  const W4Split s1 = w4_split(a.d), s2 = w4_split(a.f);
-  p1.st.m0 = {a.gate_codes, a.gate_scales, a.gate_zeros};
-  p1.st.m1 = {a.up_codes, a.up_scales, a.up_zeros};
-  p1.st.K = a.d;
-  p1.st.rows = a.f;
-  p1.st.upe = a.f / 8;
-  p1.st.passes = s1.passes;
-  p1.st.kw = s1.kw;
-  p1.st.teams = s1.teams;
-  p1.st.vec = w4_vec(a.gate_scales, a.gate_zeros, a.d, a.group) &&
-              w4_vec(a.up_scales, a.up_zeros, a.d, a.group);
-  p2.st.m0 = {a.down_codes, a.down_scales, a.down_zeros};
-  p2.st.K = a.f;
-  p2.st.rows = a.d;
-  p2.st.upe = p.units2;
-  p2.st.passes = s2.passes;
-  p2.st.kw = s2.kw;
-  p2.st.teams = s2.teams;
-  p2.st.vec = w4_vec(a.down_scales, a.down_zeros, a.f, a.group);
-  return a.f16 ? launch_g<FP16>(p1, p2, a.group, s1.warps(), s2.warps(), num_sms, s)
-               : launch_g<BF16>(p1, p2, a.group, s1.warps(), s2.warps(), num_sms, s);
+  p1.slots_cap = p2.slots_cap = w4_slots_cap(a.T, a.k, a.E, a.shared);
+  const long long n = a.E + a.shared;
+  const W4Mat gate{a.gate_codes, a.gate_scales, a.gate_zeros}, up{a.up_codes, a.up_scales, a.up_zeros};
+  if (!w4_set_stream(p1.st, gate, &up, n, a.f, a.d, a.group) ||
+      !w4_set_stream(p2.st, {a.down_codes, a.down_scales, a.down_zeros}, nullptr, n, a.d, a.f, a.group))
+    return cudaErrorInvalidValue;
+  return a.f16 ? launch_g<FP16>(p1, p2, a.group, num_sms, s) : launch_g<BF16>(p1, p2, a.group, num_sms, s);
 }
 
 }  // namespace bitmoe

@@ -317,8 +317,9 @@ typedef struct {
  *   ws: at least moe_w4_workspace_size(T, k, E, d, f, shared) bytes, 256-byte aligned; its
  *   contents need not be initialised.  Calls that may overlap on the GPU (other streams,
  *   graphs replayed side by side) need a workspace each.
- * 0 <= T <= 64; 1 <= k <= min(E, 32); 1 <= E <= 1024.  h passes between the kernels as two
- * bf16 terms (16 significant bits).  A call is deterministic. */
+ * 0 <= T <= 64; 1 <= k <= min(E, 32); 1 <= E <= 1024.  h enters the second product with
+ * 22 significant bits (and at least 2^-39 of the largest h of its 256 elements).  A call is
+ * deterministic. */
 int moe_forward_w4(const float* scores, const void* x, int T, int k, const moe_w4_weights_t* w,
                    int32_t* topk_idx, float* topk_w, float* out, void* ws, size_t ws_bytes,
                    void* stream);

@@ -2,17 +2,17 @@
 64 bits.
 
 Bounds, derived before the first run.  u = 2^-23 bounds the relative error of one fp32
-rounding in any mode (the tensor core truncates).  Every product (q - z) x is exact.
-GEMM: an element meets at most G roundings inside its group's sum, one in the scaling
-multiply-add of each of the slice's 256/G groups, one for each of the passes that add a
-warp's slices and one for each of the at most 16 warps whose sums are added, so
-  |C - C64| <= D u sum_k |x W|,   D = G + 256/G + ceil(K/4096) + 16.
+rounding in any mode.  x enters as fixed point, an element off by at most
+fx = 2^-30 max |x| over its 256 elements (fx is half a step where the largest is scaled to
+2^29 or more); the sums of q - z times that are exact.  GEMM: a group's sum meets one rounding
+to fp32, one in the scaling multiply-add of each of the slice's 256/G groups, one where its
+low and high bytes are joined, one for each pass that adds a warp's slices and one for each
+of the at most 16 warps whose sums are added, so
+  |C - C64| <= sum_k fx |W| + D u sum_k |x W|,   D = 256/G + ceil(K/4096) + 18.
 Layer: g and u as above; h = g / (1 + exp(-g)) u adds |u| |silu'(g)| dg + |silu(g)| du and
-their product, and 9 u |h| for the element-wise operations; the two bf16 terms of h leave
-2^-8 * 2^-8 |h| (a rounding to bf16 is off by at most 2^-8 of the value, the second one
-rounds the first one's rest); y = Wd h adds D u sum |Wd h| (two sums are joined: + 1 in D);
-the weights are off by at most (k + 10) u of their value (expf 2 units, the sum of k, two
-divisions), and the combine rounds once per term:
+their product, and 9 u |h| for the element-wise operations; y = Wd h adds sum fh |Wd| for h in
+fixed point and D u sum |Wd h|; the weights are off by at most (k + 10) u of their value (expf
+2 units, the sum of k, two divisions), and the combine rounds once per term:
   |out - out64| <= sum_j w_j (dy_j + (k + 10 + k + 2) u |y_j|) + dy_sh + (k + 2) u |y_sh|.
 All with a factor 1.01 for the second-order terms."""
 import pytest
@@ -52,7 +52,19 @@ def dense(codes, scales, zeros, G):
 
 
 def depth(K, G):
-    return G + 256 // G + -(-K // 4096) + 16
+    return 256 // G + -(-K // 4096) + 18
+
+
+def fixed(x):
+    """How far fixed point may be off each element."""
+    K = x.shape[1]
+    top = torch.nn.functional.pad(x.abs(), (0, -K % 256)).unflatten(1, (-1, 256)).amax(2)
+    return 2.0 ** -30 * top.repeat_interleave(256, 1)[:, :K]
+
+
+def product_bound(x, W, G):
+    """The bound on x . W^T for x and W in 64 bits."""
+    return (fixed(x) + depth(x.shape[1], G) * U * x.abs()) @ W.abs().T
 
 
 def generator(seed):
@@ -63,7 +75,7 @@ def generator(seed):
 
 def check_gemm(C, x, W, G, rows=slice(None)):
     ref = x.double() @ W.T
-    bound = 1.01 * depth(x.shape[1], G) * U * (x.double().abs() @ W.abs().T)
+    bound = 1.01 * product_bound(x.double(), W, G)
     err = (C[:, rows].double() - ref).abs()
     worst = float((err / bound.clamp_min(1e-300)).max())
     assert bool((err <= bound).all()), f"worst error is {worst:.3g} of its bound"
@@ -107,10 +119,28 @@ def test_gemm_scales_off_their_alignment(G, dtype):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype,lo,hi", [(BF, -22, 0), (FP, -14, 5), (BF, -126, -100), (BF, 90, 112)])
+def test_gemm_exact_over_the_range_of_fixed_point(dtype, lo, hi):
+    """Elements of all magnitudes that fixed point holds exactly beside the slice's largest (and
+    slices of the smallest and largest numbers): the result's error is the sums' alone."""
+    M, N, K, G = 4, 40, 512, 32
+    gen = generator(hi - lo)
+    c, s, z = weights(gen, (N, K), G, dtype, True)
+    s = (s.float() / 2 ** 4).to(dtype)
+    e = torch.randint(lo, hi + 1, (M, K), device="cuda", generator=gen).double()
+    m = 1 + torch.randint(0, 128, (M, K), device="cuda", generator=gen).double() / 128
+    x = (m * 2.0 ** e * torch.sign(torch.randn((M, K), device="cuda", generator=gen))).to(dtype)
+    C = bm.w4_gemm(x, bm.W4Matrix(c, s, z))
+    bm.sync_status()
+    W = dense(c, s, z, G)
+    err = (C.double() - x.double() @ W.T).abs()
+    assert bool((err <= 1.01 * depth(K, G) * U * (x.double().abs() @ W.abs().T)).all())
+
+
 @pytest.mark.parametrize("M", [3, 12])
 def test_gemm_rows_do_not_meet(M):
-    """inf and NaN in one row of x leave the others' bits as they were; a zero scale's group
-    adds nothing; extreme scales keep their sign and overflow to inf."""
+    """inf and NaN in one row of x leave the others' bits as they were and give what floating
+    point gives; a zero scale's group adds nothing."""
     N, K, G = 50, 544, 32
     gen = generator(7)
     c, s, z = weights(gen, (N, K), G, BF, True)
@@ -194,20 +224,17 @@ def check_layer_w4(r, x, scores, k, mats, shared, G):
             pairs.setdefault(int(idx[t, j]), []).append((t, j))
     if shared:
         pairs[E] = [(t, -1) for t in range(T)]
-    D1, f = depth(d, G), mats[0][0].shape[-2]
-    D2 = depth(f, G) + 1
     for e, tj in pairs.items():
         tok = torch.tensor([t for t, _ in tj], device="cuda")
         Wg, Wu, Wd = (dense(*(None if q is None else q[e] for q in m), G) for m in mats)
         g, u = xd[tok] @ Wg.T, xd[tok] @ Wu.T
-        dg = D1 * U * (xd[tok].abs() @ Wg.abs().T)
-        du = D1 * U * (xd[tok].abs() @ Wu.abs().T)
+        dg, du = product_bound(xd[tok], Wg, G), product_bound(xd[tok], Wu, G)
         sg = torch.sigmoid(g)
         silu, slope = g * sg, (sg * (1 + g * (1 - sg))).abs()
         h = silu * u
-        dh = u.abs() * slope * dg + silu.abs() * du + dg * du + 9 * U * h.abs() + 2.0 ** -16 * h.abs()
+        dh = u.abs() * slope * dg + silu.abs() * du + dg * du + 9 * U * h.abs()
         y = h @ Wd.T
-        dy = dh @ Wd.abs().T + D2 * U * (h.abs() @ Wd.abs().T)
+        dy = dh @ Wd.abs().T + product_bound(h, Wd, G)
         wt = torch.tensor([1.0 if j < 0 else float(w[t, j]) for t, j in tj], device="cuda",
                           dtype=torch.float64).unsqueeze(1)
         extra = torch.tensor([k + 2 if j < 0 else 2 * k + 12 for _, j in tj], device="cuda",
@@ -269,7 +296,7 @@ def test_layer_every_token_on_the_same_experts(T):
 
 
 def test_layer_tokens_do_not_meet_and_large_h_stays_finite():
-    """A token of inf and NaN leaves the others' bits alone; an h of 1e30 (past fp16) passes."""
+    """A token of inf and NaN leaves the others' bits alone; an h past fp16's range passes."""
     T, E, k, d, f, G = 6, 8, 2, 256, 128, 64
     mats, w = make_layer(8, E, d, f, G, BF, False, True)
     gen = generator(9)
