@@ -704,13 +704,14 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
   }
 }
 
-// The adding warps: the consuming warps' sums of every (unit, row pair, row of x) of a batch.  A
-// row of x has two lanes of a quad, its low and its high bytes; four threads take every fourth
-// slice each and join what they have.  `tid`: 0 .. kW4SumThreads - 1.
+// The adding warps: the consuming warps' sums of a batch, a warp a unit.  A row of x has two
+// lanes of a quad, its low and its high bytes.  Lane (sub, r) takes every fourth slice of row
+// pair r, for each row of x; the four of a row pair join what they have, and lane group `sub`
+// stores row `sub` of x.  `tid`: 0 .. kW4SumThreads - 1.
 template <typename T, typename S, int G, bool ZP, bool RING, bool DUAL, typename Job>
 __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const Job& job, int tid) {
-  constexpr int COLS = kW4Cols;
   constexpr int ROWS = DUAL ? 8 : kW4Rows;
+  const int r = tid & 7, sub = (tid >> 3) & 3, mr = w4_row<G>(r);
   const int UB = kW4Batch * p.teams, ngr = p.K / G;
   const W4Smem L = w4_smem<G, ZP, RING>(p);
   const uint32_t bars = ptx::smem_u32(smem + L.bars());
@@ -728,27 +729,29 @@ __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const J
       for (int u0 = first; u0 < first + units; u0 += UB) {
         const int nb = min(UB, first + units - u0);
         if (!w4_wait(bars + 8 * (2 * kW4MaxRing + buf), there, p, abort_flag)) return;
-        for (int i = tid; i < nb * 8 * COLS * 4; i += kW4SumThreads) {
-          const int sub = i & 3, q = i / (32 * COLS), r = (i / (4 * COLS)) & 7, c = (i / 4) % COLS;
-          const float4* at = reinterpret_cast<const float4*>(sums_at + (buf * UB + q) * p.kw * kW4Sums +
-                                                             (c >> 1) * 64 + r * 8 + (c & 1) * 4);
-          float a = 0.f, b = 0.f;
-          if (c < n_rows) {
+        for (int q = tid >> 5; q < nb; q += kW4SumThreads / 32) {
+          const float4* at = reinterpret_cast<const float4*>(sums_at + (buf * UB + q) * p.kw * kW4Sums + r * 8);
+          float a = 0.f, b = 0.f;  // of column `sub`
+#pragma unroll
+          for (int c = 0; c < kW4Cols; ++c) {
+            if (c >= n_rows) break;
+            float x = 0.f, y = 0.f;
 #pragma unroll 4
             for (int k = sub; k < p.kw; k += 4) {
-              const float4 v = at[k * (kW4Sums / 4)];
-              a += v.x + v.z;
-              b += v.y + v.w;
+              const float4 v = at[k * (kW4Sums / 4) + (c >> 1) * 16 + (c & 1)];
+              x += v.x + v.z;
+              y += v.y + v.w;
             }
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            y += __shfl_xor_sync(0xffffffffu, y, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            y += __shfl_xor_sync(0xffffffffu, y, 16);
+            if (c == sub) a = x, b = y;
           }
-          a += __shfl_xor_sync(0xffffffffu, a, 1);
-          b += __shfl_xor_sync(0xffffffffu, b, 1);
-          a += __shfl_xor_sync(0xffffffffu, a, 2);
-          b += __shfl_xor_sync(0xffffffffu, b, 2);
-          if (sub != 0 || c >= n_rows) continue;
-          const int unit = u0 + q, mr = w4_row<G>(r);
+          if (sub >= n_rows) continue;
+          const int unit = u0 + q;
           if (a != a || b != b) {
-            const typename T::Raw* x = job.row(slot, c);
+            const typename T::Raw* x = job.row(slot, sub);
             const size_t r0 = (size_t)job.matrix(slot) * p.rows + unit * ROWS + mr, r1 = DUAL ? r0 : r0 + 8;
             if (a != a && unit * ROWS + mr < p.rows)
               a = w4_slow_dot<T, S, G, ZP>(x, p.codes0 + r0 * (p.K / 2), p.scales0 + r0 * ngr, p.zeros0 + r0 * ngr, p.K);
@@ -757,7 +760,7 @@ __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const J
                                            (DUAL ? p.scales1 : p.scales0) + r1 * ngr,
                                            (DUAL ? p.zeros1 : p.zeros0) + r1 * ngr, p.K);
           }
-          job.store(slot, unit, c, mr, a, b);
+          job.store(slot, unit, sub, mr, a, b);
         }
         __syncwarp();
         if ((tid & 31) == 0) ptx::mbar_arrive(bars + 8 * (2 * kW4MaxRing + 2 + buf));
