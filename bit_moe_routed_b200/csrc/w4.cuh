@@ -40,6 +40,23 @@
 #include "waits.cuh"
 
 namespace bitmoe {
+
+// What the blocks of a stream know of its matrices.
+struct W4Stream {
+  CUtensorMap map0, map1;      // codes (w4_code_map)
+  CUtensorMap smap0, smap1;    // scales and zero points (w4_group_map), with ring_scales
+  CUtensorMap zmap0, zmap1;
+  const uint8_t *codes0, *codes1;
+  const uint16_t *scales0, *scales1;
+  const uint8_t *zeros0, *zeros1;
+  int K, rows, upe;        // rows of a matrix; units of a slot
+  int passes, kw, teams;   // the block's split (w4_split)
+  int stages;              // stages of the ring, a power of two
+  bool ring_scales;        // scales and zero points come through the ring (the kernels' RING)
+  long long wait_ns;
+  int* status;
+};
+
 namespace {
 
 constexpr int kW4Chunk = 256;      // reduction elements of a task
@@ -420,20 +437,6 @@ __device__ __noinline__ float w4_slow_dot(const typename T::Raw* x, const uint8_
 //   row(slot, col)          row `col` of x (0 .. kW4Cols - 1) in the slot, NULL past the last
 //   store(slot, unit, col, r, a, b)   the sums of rows r and r + 8 of the unit (DUAL: row r of
 //                           both matrices), by one thread
-struct W4Stream {
-  CUtensorMap map0, map1;      // codes (w4_code_map)
-  CUtensorMap smap0, smap1;    // scales and zero points (w4_group_map), with ring_scales
-  CUtensorMap zmap0, zmap1;
-  const uint8_t *codes0, *codes1;
-  const uint16_t *scales0, *scales1;
-  const uint8_t *zeros0, *zeros1;
-  int K, rows, upe;        // rows of a matrix; units of a slot
-  int passes, kw, teams;   // the block's split (w4_split)
-  int stages;              // stages of the ring, a power of two
-  bool ring_scales;        // scales and zero points come through the ring (the kernels' RING)
-  long long wait_ns;
-  int* status;
-};
 
 // Barrier of the consuming warps.
 __device__ __forceinline__ void w4_sync(const W4Stream& p) {
@@ -480,7 +483,8 @@ __device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, const W4S
 // there; left to DRAM, whose latency under load is longer than a task, they would set the pace.
 // One warp has to keep up with the memory here, a unit every 700 clocks at some 8 clocks an
 // instruction, so a unit takes as few of them as it can.
-template <int G, bool ZP, bool RING, bool DUAL, typename Job>
+// BATCH: units a team works on between two sums.
+template <int G, bool ZP, bool RING, bool DUAL, int BATCH, typename Job>
 __device__ __forceinline__ void w4_produce(const W4Stream& p, uint8_t* smem, const Job& job) {
   constexpr int ROWS = DUAL ? 8 : kW4Rows;
   const int lane = threadIdx.x & 31;
@@ -512,7 +516,7 @@ __device__ __forceinline__ void w4_produce(const W4Stream& p, uint8_t* smem, con
     for (int item = lo; item < hi && ok;) {
       const int slot = item / p.upe, first = item - slot * p.upe;
       const int units = min(p.upe - first, hi - item);
-      const int batch = p.passes > 1 ? kW4Batch * p.teams : units;
+      const int batch = p.passes > 1 ? BATCH * p.teams : units;
       for (int u0 = 0; u0 < units && ok; u0 += batch) {
         const int nb = min(batch, units - u0);
         for (int pass = 0; pass < p.passes && ok; ++pass) {
@@ -781,7 +785,7 @@ __device__ __forceinline__ bool w4_roles(const W4Stream& p, uint8_t* smem, const
   if (warp >= group) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == group) {
-      w4_produce<G, ZP, RING, DUAL>(p, smem, job);
+      w4_produce<G, ZP, RING, DUAL, kW4Batch>(p, smem, job);
     } else {
       const int tid = threadIdx.x - 32 * group - 32;
       job.before_add(tid);

@@ -5,10 +5,17 @@
 // One block a SM takes a contiguous range of items (16 rows of W times up to 4 rows of x); all of its warps share an item's reduction, so even a matrix of a few thousand rows has
 // every SM reading.  More than 4 rows of x are several slots of 4, each decoding the codes
 // again (they come from L2 by then).
-#include "w4.cuh"
+#include <type_traits>
+
+#include "w4_wide.cuh"
 
 namespace bitmoe {
 namespace {
+
+// Up to 4 rows of x take the whole-number form, more the 16-bit one, 16 rows a slot (8192 x
+// 4096, G = 128: see the table of both beside kW4WholeRows' use).
+constexpr int kW4WholeRows = 4;
+constexpr int kW4WideRows = 16;
 
 struct W4GemmParams {
   W4Stream st;
@@ -17,6 +24,8 @@ struct W4GemmParams {
   int M, slots;
 };
 
+// COLS: rows of x in a slot.
+template <int COLS>
 struct GemmJob {
   const W4GemmParams& p;
   __device__ __forceinline__ void range(int part, int& lo, int& hi) const {
@@ -28,13 +37,13 @@ struct GemmJob {
   template <typename Wait>
   __device__ __forceinline__ bool plan(Wait) const { return true; }
   __device__ __forceinline__ bool same_rows() const { return false; }
-  __device__ __forceinline__ int rows(int slot) const { return min(kW4Cols, p.M - slot * kW4Cols); }
+  __device__ __forceinline__ int rows(int slot) const { return min(COLS, p.M - slot * COLS); }
   __device__ __forceinline__ const uint16_t* row(int slot, int col) const {
-    const int m = slot * kW4Cols + col;
+    const int m = slot * COLS + col;
     return m < p.M ? p.x + (size_t)m * p.st.K : nullptr;
   }
   __device__ __forceinline__ void store(int slot, int unit, int col, int r, float a, float b) const {
-    const int m = slot * kW4Cols + col, n = unit * kW4Rows + r;
+    const int m = slot * COLS + col, n = unit * kW4Rows + r;
     if (m >= p.M) return;
     float* c = p.C + (size_t)m * p.st.rows + n;
     if (n < p.st.rows) c[0] = a;
@@ -50,13 +59,25 @@ __global__ void __launch_bounds__(kW4MaxThreads, 1) w4_gemm_kernel(const __grid_
   uint8_t* smem = w4_raw + ((1024 - (ptx::smem_u32(w4_raw) & 1023)) & 1023);
   w4_init(p.st, smem, w4_smem<G, ZP, RING>(p.st));
   __syncthreads();
-  GemmJob job{p};
+  GemmJob<kW4Cols> job{p};
   if (w4_roles<T, T, G, ZP, RING, false>(p.st, smem, job)) w4_consume<T, T, G, ZP, RING, false>(p.st, smem, job);
+}
+
+template <typename T, typename O, int G, bool ZP, bool RING>
+__global__ void __launch_bounds__(kW4MaxThreads, 1) w4_gemm_wide_kernel(const __grid_constant__ W4GemmParams p) {
+  extern __shared__ uint8_t w4_raw[];
+  uint8_t* smem = w4_raw + ((1024 - (ptx::smem_u32(w4_raw) & 1023)) & 1023);
+  w4_init(p.st, smem, w4_smem<G, ZP, RING>(p.st));
+  __syncthreads();
+  GemmJob<kW4WideRows> job{p};
+  if (w4_roles_wide<T, G, ZP, RING, false>(p.st, smem, job))
+    w4_consume_wide<O, T, T, G, ZP, RING, false>(p.st, smem, job);
 }
 
 template <typename T, int G, bool ZP, bool RING>
 cudaError_t launch_one(const W4GemmParams& p, int blocks, int warps, cudaStream_t s) {
-  auto kern = w4_gemm_kernel<T, G, ZP, RING>;
+  using O = std::conditional_t<std::is_same_v<T, FP16>, WideFP16, WideBF16>;
+  auto kern = p.M > kW4WholeRows ? w4_gemm_wide_kernel<T, O, G, ZP, RING> : w4_gemm_kernel<T, G, ZP, RING>;
   const size_t smem = (size_t)w4_smem<G, ZP, RING>(p.st).bytes() + kW4SmemPad;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -88,7 +109,8 @@ cudaError_t launch_w4_gemm(const W4GemmLaunch& a, cudaStream_t s, int num_sms) {
   p.x = a.x;
   p.C = a.C;
   p.M = a.M;
-  p.slots = (a.M + kW4Cols - 1) / kW4Cols;
+  const int cols = a.M > kW4WholeRows ? kW4WideRows : kW4Cols;
+  p.slots = (a.M + cols - 1) / cols;
   const long long total = (long long)p.slots * p.st.upe;
   const int warps = p.st.kw * p.st.teams;
   const int blocks = (int)(total < num_sms ? total : num_sms);
