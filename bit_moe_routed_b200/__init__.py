@@ -494,7 +494,7 @@ def w4_gemm(x: torch.Tensor, w: W4Matrix, out: torch.Tensor | None = None, strea
     _fits("x", x, (M, K), w.dtype, dev)
     s = _w4_stream(dev, stream)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=dev)
+        out = torch.empty(M, N, dtype=torch.float32, device=dev)
     else:
         _fits("out", out, (M, N), torch.float32, dev)
     _check((_lib or lib()).moe_w4_gemm(x.data_ptr(), w._dtype_code, M, w._struct, N, K, w.group,
@@ -531,7 +531,7 @@ def forward_w4(x: torch.Tensor, scores: torch.Tensor, k: int, w: W4Layer,
                                ("out", (T, w.d), torch.float32)):
         t = outs.get(name) if outs is not None else None
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = torch.empty(*shape, dtype=dtype, device=dev)
         else:
             _fits(name, t, shape, dtype, dev)
         o[name] = t

@@ -35,6 +35,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "internal.cuh"
 #include "ptx.cuh"
 #include "waits.cuh"
@@ -796,6 +798,18 @@ __device__ __forceinline__ bool w4_roles(const W4Stream& p, uint8_t* smem, const
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
   return warp < warps;
+}
+
+// Allows a kernel a SM's whole shared memory, once a device (bit `device` of `allowed`).
+constexpr int kW4MaxSmem = 227 * 1024;
+template <typename Kernel>
+cudaError_t w4_allow_smem(Kernel kern, std::atomic<unsigned long long>& allowed) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (allowed.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4MaxSmem);
+  if (e == cudaSuccess) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
 }
 
 // Host side: the map of a matrix's codes, [matrices * rows][K/2] bytes, with the 128-byte

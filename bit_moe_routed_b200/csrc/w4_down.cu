@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kW4MaxThreads, 1) w4_down_kernel(const __grid_
 template <typename S, int G, bool ZP, bool RING, bool WIDE>
 struct DownLaunch {
   static cudaError_t run(const W4LayerParams& p, int blocks, cudaStream_t s) {
-    return w4_launch<G, ZP, RING>(w4_down_kernel<S, G, ZP, RING, WIDE>, p, true, blocks, s);
+    return w4_launch<DownLaunch, G, ZP, RING>(w4_down_kernel<S, G, ZP, RING, WIDE>, p, true, blocks, s);
   }
 };
 

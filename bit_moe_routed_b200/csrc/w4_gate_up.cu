@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kW4MaxThreads, 1) w4_gate_up_kernel(const __gr
 template <typename T, int G, bool ZP, bool RING, bool WIDE>
 struct GateUpLaunch {
   static cudaError_t run(const W4LayerParams& p, int blocks, cudaStream_t s) {
-    return w4_launch<G, ZP, RING>(w4_gate_up_kernel<T, G, ZP, RING, WIDE>, p, false, blocks, s);
+    return w4_launch<GateUpLaunch, G, ZP, RING>(w4_gate_up_kernel<T, G, ZP, RING, WIDE>, p, false, blocks, s);
   }
 };
 

@@ -79,7 +79,8 @@ cudaError_t launch_one(const W4GemmParams& p, int blocks, int warps, cudaStream_
   using O = std::conditional_t<std::is_same_v<T, FP16>, WideFP16, WideBF16>;
   auto kern = p.M > kW4WholeRows ? w4_gemm_wide_kernel<T, O, G, ZP, RING> : w4_gemm_kernel<T, G, ZP, RING>;
   const size_t smem = (size_t)w4_smem<G, ZP, RING>(p.st).bytes() + kW4SmemPad;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> allowed[2];
+  cudaError_t e = w4_allow_smem(kern, allowed[p.M > kW4WholeRows]);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)w4_threads(warps)), smem, s, false, p);
 }

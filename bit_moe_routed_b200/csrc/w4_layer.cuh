@@ -211,15 +211,23 @@ __device__ __forceinline__ void w4_plan_few(const W4LayerParams& p, const W4Plan
   }
 }
 
-// What both kernels' jobs share: the slots, and the block's items: its share of the shared
-// expert's (which the copying warp can start on before the routing is known) and the rest.
+// What both kernels' jobs share: the slots, and the block's items.  Kernel 1 takes its share of
+// the shared expert's units first, which needs no routing; kernel 2, whose routing is done by
+// the time that kernel 1 has finished, one run of everything (a slot less to load h for).
 struct LayerJob {
   const W4LayerParams& p;
   W4Plan L;
   uint8_t* scratch;  // for w4_plan_few
   uint32_t ready;    // barrier: the slots are known
-  __device__ __forceinline__ void range(int part, int& lo, int& hi) const {
-    // at most 2^22 items: 32 bits hold the products
+  // at most 2^22 items: 32 bits hold the products
+  __device__ __forceinline__ void whole_range(int part, int& lo, int& hi) const {
+    lo = hi = 0;
+    if (part == 0) return;
+    const unsigned all = (unsigned)(*L.total * p.st.upe), G = gridDim.x, b = blockIdx.x;
+    lo = (int)(b * all / G);
+    hi = (int)((b + 1) * all / G);
+  }
+  __device__ __forceinline__ void shared_first_range(int part, int& lo, int& hi) const {
     const unsigned S = (unsigned)(p.shared_slots * p.st.upe), G = gridDim.x, b = blockIdx.x;
     const unsigned s0 = b * S / G, s1 = (b + 1) * S / G;
     lo = (int)s0;
@@ -254,6 +262,7 @@ __device__ __forceinline__ int w4_atom_add_acq_rel(int* p, int v) {
 }
 
 struct GateUpJob : LayerJob {
+  __device__ __forceinline__ void range(int part, int& lo, int& hi) const { shared_first_range(part, lo, hi); }
   __device__ __forceinline__ const uint16_t* row(int slot, int col) const {
     if (col >= rows(slot)) return nullptr;
     const int pr = pair(slot, col);
@@ -299,6 +308,7 @@ constexpr int kW4InlineT = 8;
 struct DownJob : LayerJob {
   int* list;   // [units2], in memory that the stream has finished with
   int* count;  // 0 at the start
+  __device__ __forceinline__ void range(int part, int& lo, int& hi) const { whole_range(part, lo, hi); }
   __device__ __forceinline__ const float* row(int slot, int col) const {
     return col < rows(slot) ? p.h + (size_t)pair(slot, col) * p.f : nullptr;
   }
@@ -317,13 +327,11 @@ struct DownJob : LayerJob {
     if (p.T > kW4InlineT) return;
     const int threads = p.st.kw * p.st.teams * 32 + kW4SumThreads;
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");  // every store
-    for (int part = 0; part < 2; ++part) {
-      int lo, hi;
-      range(part, lo, hi);
-      for (int i = lo + tid; i < hi; i += threads) {
-        const int u = i % p.st.upe;
-        if (w4_atom_add_acq_rel(p.cnt + u, 1) == *L.total - 1) list[atomicAdd(count, 1)] = u;
-      }
+    int lo, hi;
+    range(1, lo, hi);
+    for (int i = lo + tid; i < hi; i += threads) {
+      const int u = i % p.st.upe;
+      if (w4_atom_add_acq_rel(p.cnt + u, 1) == *L.total - 1) list[atomicAdd(count, 1)] = u;
     }
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
     const int work = *count * p.T * 4;
@@ -362,10 +370,12 @@ template <template <typename, int, bool, bool, bool> class F>
 cudaError_t w4_pick(bool f16, int group, bool wide, const W4LayerParams& p, int blocks, cudaStream_t s) {
   return f16 ? w4_pick_g<F, FP16>(group, wide, p, blocks, s) : w4_pick_g<F, BF16>(group, wide, p, blocks, s);
 }
-template <int G, bool ZP, bool RING, typename Kernel>
+// Id: a type of the kernel's own, so that each has its `allowed`.
+template <typename Id, int G, bool ZP, bool RING, typename Kernel>
 cudaError_t w4_launch(Kernel kern, const W4LayerParams& p, bool overlap, int blocks, cudaStream_t s) {
   const size_t smem = w4_smem<G, ZP, RING>(p.st).bytes() + w4_plan_smem(p) + kW4SmemPad;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = w4_allow_smem(kern, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)w4_threads(p.st.kw * p.st.teams)), smem, s, overlap, p);
 }
