@@ -225,22 +225,6 @@ struct W4RowScales {
   static constexpr int NG = kW4Chunk / G;  // groups in a slice: 2, 4, 8
   uint32_t s[NG / 2];
   uint32_t z[NG == 8 ? 2 : 1];
-  // from memory, `valid` groups one by one
-  __device__ __forceinline__ void load(const uint16_t* sp, const uint8_t* zp, int valid) {
-#pragma unroll
-    for (int i = 0; i < NG / 2; ++i) {
-      const uint32_t lo = 2 * i < valid ? __ldg(sp + 2 * i) : 0u;
-      const uint32_t hi = 2 * i + 1 < valid ? __ldg(sp + 2 * i + 1) : 0u;
-      s[i] = lo | (hi << 16);
-    }
-    if constexpr (ZP) {
-      z[0] = 0;
-      if constexpr (NG == 8) z[1] = 0;
-#pragma unroll
-      for (int i = 0; i < NG; ++i)
-        if (i < valid) z[i / 4] |= (uint32_t)__ldg(zp + i) << (8 * (i % 4));
-    }
-  }
   // from a stage of the ring
   __device__ __forceinline__ void load_ring(uint32_t sp, uint32_t zp) {
     w4_lds(sp, s);
@@ -256,6 +240,41 @@ struct W4RowScales {
     return S::to_float((b & 1) ? s[b / 2] >> 16 : s[b / 2] & 0xFFFFu);
   }
   __device__ __forceinline__ int zero(int b) const { return (int)((z[b / 4] >> (8 * (b % 4))) & 0x7Fu); }
+};
+// A lane's quarter of them (two groups, one, or of two groups one), loaded from memory at any
+// alignment; the quad puts them together where they are used.
+template <int G, bool ZP>
+struct W4Quarter {
+  static constexpr int NG = kW4Chunk / G;
+  uint32_t s = 0, z = 0;
+  __device__ __forceinline__ void load(const uint16_t* sp, const uint8_t* zp, int valid, int t) {
+    const int i = NG == 8 ? 2 * t : NG == 4 ? t : t & 1;
+    s = i < valid ? __ldg(sp + i) : 0u;
+    if (NG == 8 && i + 1 < valid) s |= (uint32_t)__ldg(sp + i + 1) << 16;
+    if constexpr (ZP) {
+      z = i < valid ? __ldg(zp + i) : 0u;
+      if (NG == 8 && i + 1 < valid) z |= (uint32_t)__ldg(zp + i + 1) << 8;
+    }
+  }
+  __device__ __forceinline__ void whole(W4RowScales<G, ZP>& r, int lane) const {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < (NG == 2 ? 2 : 4); ++i) v[i] = __shfl_sync(0xffffffffu, s, (lane & 28) | i);
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) r.s[i] = NG == 8 ? v[i] : ptx::prmt(v[2 * i], v[2 * i + 1], 0x5410);
+    if constexpr (ZP) {
+#pragma unroll
+      for (int i = 0; i < (NG == 2 ? 2 : 4); ++i) v[i] = __shfl_sync(0xffffffffu, z, (lane & 28) | i);
+      if constexpr (NG == 8) {
+        r.z[0] = ptx::prmt(v[0], v[1], 0x5410);
+        r.z[1] = ptx::prmt(v[2], v[3], 0x5410);
+      } else if constexpr (NG == 4) {
+        r.z[0] = ptx::prmt(ptx::prmt(v[0], v[1], 0x0040), ptx::prmt(v[2], v[3], 0x0040), 0x5410);
+      } else {
+        r.z[0] = ptx::prmt(v[0], v[1], 0x0040);
+      }
+    }
+  }
 };
 
 // One task: 16 rows times the B sets, group by group; `at` is the lane's group 0 in the first
@@ -634,15 +653,15 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
         const int left = p.K - chunk * kW4Chunk;
         const int valid = left <= 0 ? 0 : min(left, kW4Chunk) / G;  // groups of this slice
         // scales that do not come through the ring: the first unit's, then one task ahead
-        W4RowScales<G, ZP> next0{}, next1{};
+        W4Quarter<G, ZP> next0, next1;
         size_t at0 = 0;
         int rows_left = 0;
         auto load_scales = [&](int q) {
           if (q >= nb || valid == 0) return;
           const size_t at1 = DUAL ? at0 : at0 + (size_t)8 * ngr;
-          if (!RAGGED || rows_left > 0) next0.load(p.scales0 + at0, p.zeros0 + at0, valid);
+          if (!RAGGED || rows_left > 0) next0.load(p.scales0 + at0, p.zeros0 + at0, valid, t);
           if (!RAGGED || rows_left > 8)
-            next1.load((DUAL ? p.scales1 : p.scales0) + at1, (DUAL ? p.zeros1 : p.zeros0) + at1, valid);
+            next1.load((DUAL ? p.scales1 : p.scales0) + at1, (DUAL ? p.zeros1 : p.zeros0) + at1, valid, t);
           at0 += step;
           if (RAGGED) rows_left -= p.teams * ROWS;
         };
@@ -666,7 +685,7 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
         }
         float* sums = sums_at + ((buf * UB + team) * p.kw + kw) * kW4Sums + lane * 2;
         for (int q = team; q < nb; q += p.teams, sums += p.teams * p.kw * kW4Sums) {
-          W4RowScales<G, ZP> r0 = next0, r1 = next1;
+          const W4Quarter<G, ZP> now0 = next0, now1 = next1;
           if (!RING) load_scales(q + p.teams);
           const int seq = seq0 + q, stage = seq & (p.stages - 1);
           const uint32_t parity = (uint32_t)(seq / p.stages) & 1u;
@@ -675,7 +694,11 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
           float tot[kW4Sets][2];
           const uint32_t at = lane_at + stage * stage_bytes;
           if (valid > 0) {  // as many sets as the slot has rows for
-            if (RING) {
+            W4RowScales<G, ZP> r0, r1;
+            if (!RING) {
+              now0.whole(r0, lane);
+              now1.whole(r1, lane);
+            } else {
               const uint32_t zp = lane_zp + stage * zstage, sp = lane_sp + stage * (2 * zstage);
               r0.load_ring(sp, zp);
               r1.load_ring(sp + 16 * gpitch, zp + 8 * gpitch);

@@ -20,7 +20,8 @@ __global__ void __launch_bounds__(kW4MaxThreads, 1) w4_down_kernel(const __grid_
   w4_init(p.st, smem, M);
   const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * (2 * kW4MaxRing + 4);
   DownJob job{{p, w4_plan_at(p, smem + M.bytes()), smem + M.few(), ready},
-                               reinterpret_cast<int*>(smem), reinterpret_cast<int*>(smem + M.counter())};
+                               reinterpret_cast<int*>(smem), reinterpret_cast<int*>(smem + M.counter()),
+              reinterpret_cast<const volatile int*>(smem + M.abort_flag())};
   __syncthreads();
   if (!(WIDE ? w4_roles_wide<FP32, G, ZP, RING, false>(p.st, smem, job)
              : w4_roles<FP32, S, G, ZP, RING, false>(p.st, smem, job)))

@@ -211,9 +211,12 @@ __device__ __forceinline__ void w4_plan_few(const W4LayerParams& p, const W4Plan
   }
 }
 
-// What both kernels' jobs share: the slots, and the block's items.  Kernel 1 takes its share of
-// the shared expert's units first, which needs no routing; kernel 2, whose routing is done by
-// the time that kernel 1 has finished, one run of everything (a slot less to load h for).
+// What both kernels' jobs share: the slots, and the block's items.  A block takes its share of
+// the shared expert's units first: that needs no routing, and those units, with the most rows
+// of x, are spread evenly.  Up to 2 tokens all units cost the same and kernel 2, whose routing is
+// done by the time that kernel 1 has finished, takes one run of everything, a slot less to load
+// h for (1 token, d = f = 512: 20 us a layer against 23; 4 tokens, d = 4096, f = 2048: 120
+// against 111, so there the shared units stay first).
 struct LayerJob {
   const W4LayerParams& p;
   W4Plan L;
@@ -308,7 +311,13 @@ constexpr int kW4InlineT = 8;
 struct DownJob : LayerJob {
   int* list;   // [units2], in memory that the stream has finished with
   int* count;  // 0 at the start
-  __device__ __forceinline__ void range(int part, int& lo, int& hi) const { whole_range(part, lo, hi); }
+  const volatile int* aborted;  // a wait of the block has run out: nothing to add up
+  __device__ __forceinline__ void range(int part, int& lo, int& hi) const {
+    if (p.T <= kW4SetRows)
+      whole_range(part, lo, hi);
+    else
+      shared_first_range(part, lo, hi);
+  }
   __device__ __forceinline__ const float* row(int slot, int col) const {
     return col < rows(slot) ? p.h + (size_t)pair(slot, col) * p.f : nullptr;
   }
@@ -327,11 +336,14 @@ struct DownJob : LayerJob {
     if (p.T > kW4InlineT) return;
     const int threads = p.st.kw * p.st.teams * 32 + kW4SumThreads;
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");  // every store
-    int lo, hi;
-    range(1, lo, hi);
-    for (int i = lo + tid; i < hi; i += threads) {
-      const int u = i % p.st.upe;
-      if (w4_atom_add_acq_rel(p.cnt + u, 1) == *L.total - 1) list[atomicAdd(count, 1)] = u;
+    if (*aborted) return;
+    for (int part = 0; part < 2; ++part) {
+      int lo, hi;
+      range(part, lo, hi);
+      for (int i = lo + tid; i < hi; i += threads) {
+        const int u = i % p.st.upe;
+        if (w4_atom_add_acq_rel(p.cnt + u, 1) == *L.total - 1) list[atomicAdd(count, 1)] = u;
+      }
     }
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
     const int work = *count * p.T * 4;

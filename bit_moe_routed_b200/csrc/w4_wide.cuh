@@ -215,13 +215,13 @@ __device__ __forceinline__ void w4_consume_wide(const W4Stream& p, uint8_t* smem
         const int chunk = pass * p.kw + kw;
         const int left = p.K - chunk * kW4Chunk;
         const int valid = left <= 0 ? 0 : min(left, kW4Chunk) / G;
-        W4RowScales<G, ZP> r0{}, r1{};
+        W4Quarter<G, ZP> quarter0, quarter1;
         if (!RING && valid > 0) {
           const int r = (u0 + team) * ROWS + row;
           const size_t at0 = (size_t)(base + r) * ngr + (size_t)chunk * NG, at1 = DUAL ? at0 : at0 + (size_t)8 * ngr;
-          if (!RAGGED || r < p.rows) r0.load(p.scales0 + at0, p.zeros0 + at0, valid);
+          if (!RAGGED || r < p.rows) quarter0.load(p.scales0 + at0, p.zeros0 + at0, valid, t);
           if (!RAGGED || r + 8 < p.rows)
-            r1.load((DUAL ? p.scales1 : p.scales0) + at1, (DUAL ? p.zeros1 : p.zeros0) + at1, valid);
+            quarter1.load((DUAL ? p.scales1 : p.scales0) + at1, (DUAL ? p.zeros1 : p.zeros0) + at1, valid, t);
         }
         if (valid > 0 && (p.passes > 1 || u0 == first)) {
           if constexpr (TERMS) {
@@ -243,7 +243,11 @@ __device__ __forceinline__ void w4_consume_wide(const W4Stream& p, uint8_t* smem
         const uint32_t at = lane_at + stage * stage_bytes;
         float tot[kW4WideSets][4];
         if (valid > 0) {
-          if (RING) {
+          W4RowScales<G, ZP> r0, r1;
+          if (!RING) {
+            quarter0.whole(r0, lane);
+            quarter1.whole(r1, lane);
+          } else {
             const uint32_t zp = lane_zp + stage * zstage, sp = lane_sp + stage * (2 * zstage);
             r0.load_ring(sp, zp);
             r1.load_ring(sp + 16 * gpitch, zp + 8 * gpitch);

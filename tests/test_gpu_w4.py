@@ -408,3 +408,29 @@ def test_a_decode_step_through_router_layers_and_head(dtype):
     logits = bm.w4_gemm(hidden, bm.W4Matrix(*head))
     bm.sync_status()
     check_gemm(logits, hidden, dense(*head, G), G)
+
+
+def test_expired_waits_are_reported_and_recoverable():
+    """With a limit of 1 ns the kernels' waits run out: the status reports it (or every copy was
+    there in time), the calls return, and the next call is right."""
+    T, E, k, d, f, G = 6, 12, 3, 1024, 512, 64
+    mats, w = make_layer(41, E, d, f, G, BF, True, True)
+    gen = generator(42)
+    x = torch.randn((T, d), device="cuda", generator=gen).to(BF)
+    s = torch.randn((T, E), device="cuda", generator=gen)
+    m = weights(gen, (500, d), G, BF, True)
+    bm.sync_status()
+    bm.set_wait_limit_ns(1)
+    try:
+        for call in (lambda: bm.forward_w4(x, s, k, w), lambda: bm.forward_w4(x[:1], s[:1], k, w),
+                     lambda: bm.w4_gemm(x, bm.W4Matrix(*m)), lambda: bm.w4_gemm(x[:2], bm.W4Matrix(*m))):
+            call()
+            try:
+                bm.sync_status()
+            except bm.MoeError as e:
+                assert e.code == bm.MOE_ERR_TIMEOUT
+    finally:
+        bm.set_wait_limit_ns(0)
+    bm.sync_status()
+    check_layer_w4(bm.forward_w4(x, s, k, w), x, s, k, mats, True, G)
+    check_gemm(bm.w4_gemm(x, bm.W4Matrix(*m)), x, dense(*m, G), G)
