@@ -21,7 +21,7 @@
 //     256 elements for all its tasks, so the B operand, up to 4 rows of x in that slice, sits
 //     in 16 registers per two rows for the whole slot;
 //   - one warp of its own brings a unit (16 rows) for all the warps that share it with one or
-//     two TMA boxes of up to 32 KB into a ring of 128 KB; it alone walks the list of units;
+//     two TMA boxes of up to 32 KB into a ring of 64 KB; it alone walks the list of units;
 //   - within a group, lane t of a quad takes a quarter of the group's elements (its 4, 8 or
 //     16 bytes of codes) whichever k those are: the k order inside a dot product is free as
 //     long as A and B agree, and this one makes the fragment a straight read of the row;
@@ -63,7 +63,7 @@ namespace {
 
 constexpr int kW4Chunk = 256;      // reduction elements of a task
 constexpr int kW4Rows = 16;        // rows of a task (the MMA's M)
-constexpr int kW4Stages = 4;       // units under way per team of warps
+constexpr int kW4Stages = 2;       // units under way per team of warps (4: the same times)
 constexpr int kW4StageBytes = kW4Rows * kW4Chunk / 2;
 constexpr int kW4MaxWarps = 16;
 constexpr int kW4SetRows = 2;      // rows of x per B set: 4 bytes each fill the MMA's 8 columns
@@ -87,10 +87,12 @@ inline W4Split w4_split(int K) {
   return s;
 }
 // Shared memory of a block of W consuming warps: the ring of codes (at a 1024-byte boundary),
-// of scales and of zero points, two buffers of partial sums, the sums of x's bytes, the barriers, the abort flag and a
+// of scales and of zero points, the buffers of partial sums, the sums of bytes of x, the barriers, the abort flag and a
 // counter; what the kernel adds comes after.
 constexpr int kW4MaxRing = kW4Stages * kW4MaxWarps;  // most stages (one warp a unit)
-constexpr int kW4PartBytes = 1024;                   // of a warp in one buffer of sums
+constexpr int kW4Bufs = 4;                           // buffers of partial sums
+constexpr int kW4PartBytes = 1024;                   // of a warp in one of them
+constexpr int kW4BarSums = 2 * kW4MaxRing, kW4BarTaken = kW4BarSums + kW4Bufs, kW4BarPlan = kW4BarTaken + kW4Bufs;
 constexpr int kW4ByteSums = 512;                     // of a warp's sums of x's bytes (two sets)
 struct W4Smem {
   int warps, groups;  // groups: per slice, 0 where scales do not come through the ring
@@ -98,9 +100,9 @@ struct W4Smem {
   __host__ __device__ int scales() const { return warps * kW4Stages * kW4StageBytes; }
   __host__ __device__ int zero_points() const { return scales() + warps * kW4Stages * groups * kW4Rows * 2; }
   __host__ __device__ int part() const { return zero_points() + (zeros ? warps * kW4Stages * groups * kW4Rows : 0); }
-  __host__ __device__ int byte_sums() const { return part() + warps * 2 * kW4PartBytes; }
+  __host__ __device__ int byte_sums() const { return part() + warps * kW4Bufs * kW4PartBytes; }
   __host__ __device__ int bars() const { return byte_sums() + (zeros ? warps * kW4ByteSums : 0); }
-  __host__ __device__ int abort_flag() const { return bars() + (2 * kW4MaxRing + 5) * 8; }
+  __host__ __device__ int abort_flag() const { return bars() + (kW4BarPlan + 1) * 8; }
   __host__ __device__ int counter() const { return abort_flag() + 4; }
   __host__ __device__ int few() const { return abort_flag() + 16; }  // scratch of the adding warps
   __host__ __device__ int bytes() const { return few() + 1024; }
@@ -476,11 +478,11 @@ __device__ __forceinline__ void w4_init(const W4Stream& p, uint8_t* smem, const 
     ptx::mbar_init(bars + 8 * (kW4MaxRing + i), p.kw);  // empty: the warps of a unit
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bars + 8 * (2 * kW4MaxRing + i), L.warps);                 // sums there
-      ptx::mbar_init(bars + 8 * (2 * kW4MaxRing + 2 + i), kW4SumThreads / 32);  // sums taken
+    for (int i = 0; i < kW4Bufs; ++i) {
+      ptx::mbar_init(bars + 8 * (kW4BarSums + i), L.warps);                 // sums there
+      ptx::mbar_init(bars + 8 * (kW4BarTaken + i), kW4SumThreads / 32);  // sums taken
     }
-    ptx::mbar_init(bars + 8 * (2 * kW4MaxRing + 4), 1);  // the slots are known
+    ptx::mbar_init(bars + 8 * kW4BarPlan, 1);  // the slots are known
     *reinterpret_cast<int*>(smem + L.abort_flag()) = 0;
     *reinterpret_cast<int*>(smem + L.counter()) = 0;
   }
@@ -532,7 +534,7 @@ __device__ __forceinline__ void w4_produce(const W4Stream& p, uint8_t* smem, con
   bool ok = true;
   for (int part = 0; part < 2; ++part) {
     int lo, hi;
-    if (part == 1 && !job.plan([&] { return w4_wait(bars + 8 * (2 * kW4MaxRing + 4), 0, p, abort_flag); })) break;
+    if (part == 1 && !job.plan([&] { return w4_wait(bars + 8 * kW4BarPlan, 0, p, abort_flag); })) break;
     job.range(part, lo, hi);
     for (int item = lo; item < hi && ok;) {
       const int slot = item / p.upe, first = item - slot * p.upe;
@@ -638,7 +640,7 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
   for (int part = 0, item = lo; part < 2;) {
     if (item >= hi) {
       if (++part == 2) break;
-      if (!job.plan([&] { return w4_wait(bars + 8 * (2 * kW4MaxRing + 4), 0, p, abort_flag); })) break;
+      if (!job.plan([&] { return w4_wait(bars + 8 * kW4BarPlan, 0, p, abort_flag); })) break;
       job.range(1, item, hi);
       continue;
     }
@@ -647,7 +649,7 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
     const int base = job.matrix(slot) * p.rows;
     for (int u0 = first; u0 < first + units; u0 += UB) {
       const int nb = min(UB, first + units - u0);
-      if (ok) ok = w4_wait(bars + 8 * (2 * kW4MaxRing + 2 + buf), taken, p, abort_flag);
+      if (ok) ok = w4_wait(bars + 8 * (kW4BarTaken + buf), taken, p, abort_flag);
       for (int pass = 0; pass < p.passes; ++pass, seq0 += nb) {
         const int chunk = pass * p.kw + kw;
         const int left = p.K - chunk * kW4Chunk;
@@ -725,8 +727,8 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + 8 * (2 * kW4MaxRing + buf));
-      buf ^= 1;
+      if (lane == 0) ptx::mbar_arrive(bars + 8 * (kW4BarSums + buf));
+      buf = (buf + 1) % kW4Bufs;
       if (buf == 0) taken ^= 1;
     }
     item += units;
@@ -750,14 +752,14 @@ __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const J
   uint32_t there = 0;
   for (int part = 0; part < 2; ++part) {
     int lo, hi;
-    if (part == 1 && !job.plan([&] { return w4_wait(bars + 8 * (2 * kW4MaxRing + 4), 0, p, abort_flag); })) return;
+    if (part == 1 && !job.plan([&] { return w4_wait(bars + 8 * kW4BarPlan, 0, p, abort_flag); })) return;
     job.range(part, lo, hi);
     for (int item = lo; item < hi;) {
       const int slot = item / p.upe, first = item - slot * p.upe;
       const int units = min(p.upe - first, hi - item), n_rows = job.rows(slot);
       for (int u0 = first; u0 < first + units; u0 += UB) {
         const int nb = min(UB, first + units - u0);
-        if (!w4_wait(bars + 8 * (2 * kW4MaxRing + buf), there, p, abort_flag)) return;
+        if (!w4_wait(bars + 8 * (kW4BarSums + buf), there, p, abort_flag)) return;
         for (int q = tid >> 5; q < nb; q += kW4SumThreads / 32) {
           const float4* at = reinterpret_cast<const float4*>(sums_at + (buf * UB + q) * p.kw * kW4Sums + r * 8);
           float a = 0.f, b = 0.f;  // of column `sub`
@@ -792,8 +794,8 @@ __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const J
           job.store(slot, unit, sub, mr, a, b);
         }
         __syncwarp();
-        if ((tid & 31) == 0) ptx::mbar_arrive(bars + 8 * (2 * kW4MaxRing + 2 + buf));
-        buf ^= 1;
+        if ((tid & 31) == 0) ptx::mbar_arrive(bars + 8 * (kW4BarTaken + buf));
+        buf = (buf + 1) % kW4Bufs;
         if (buf == 0) there ^= 1;
       }
       item += units;

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(kW4MaxThreads, 1) w4_down_kernel(const __grid_
   ptx::griddep_launch_dependents();
   const W4Smem M = w4_smem<G, ZP, RING>(p.st);
   w4_init(p.st, smem, M);
-  const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * (2 * kW4MaxRing + 4);
+  const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * kW4BarPlan;
   DownJob job{{p, w4_plan_at(p, smem + M.bytes()), smem + M.few(), ready},
                                reinterpret_cast<int*>(smem), reinterpret_cast<int*>(smem + M.counter()),
               reinterpret_cast<const volatile int*>(smem + M.abort_flag())};

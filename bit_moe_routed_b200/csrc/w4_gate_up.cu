@@ -12,7 +12,7 @@ __global__ void __launch_bounds__(kW4MaxThreads, 1) w4_gate_up_kernel(const __gr
   ptx::griddep_launch_dependents();
   const W4Smem M = w4_smem<G, ZP, RING>(p.st);
   w4_init(p.st, smem, M);
-  const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * (2 * kW4MaxRing + 4);
+  const uint32_t ready = ptx::smem_u32(smem + M.bars()) + 8 * kW4BarPlan;
   GateUpJob job{{p, w4_plan_at(p, smem + M.bytes()), smem + M.few(), ready}};
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.units2; i += blockDim.x) p.cnt[i] = 0;

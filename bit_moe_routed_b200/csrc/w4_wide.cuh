@@ -200,7 +200,7 @@ __device__ __forceinline__ void w4_consume_wide(const W4Stream& p, uint8_t* smem
   for (int part = 0, item = lo; part < 2;) {
     if (item >= hi) {
       if (++part == 2) break;
-      if (!job.plan([&] { return w4_wait(bars + 8 * (2 * kW4MaxRing + 4), 0, p, abort_flag); })) break;
+      if (!job.plan([&] { return w4_wait(bars + 8 * kW4BarPlan, 0, p, abort_flag); })) break;
       job.range(1, item, hi);
       continue;
     }
@@ -209,7 +209,7 @@ __device__ __forceinline__ void w4_consume_wide(const W4Stream& p, uint8_t* smem
     const int base = job.matrix(slot) * p.rows;
     for (int u0 = first; u0 < first + units; u0 += UB) {
       const int nb = min(UB, first + units - u0);
-      if (ok) ok = w4_wait(bars + 8 * (2 * kW4MaxRing + 2 + buf), taken, p, abort_flag);
+      if (ok) ok = w4_wait(bars + 8 * (kW4BarTaken + buf), taken, p, abort_flag);
       for (int pass = 0; pass < p.passes; ++pass, seq0 += nb) {
         if (team >= nb) continue;
         const int chunk = pass * p.kw + kw;
@@ -277,8 +277,8 @@ __device__ __forceinline__ void w4_consume_wide(const W4Stream& p, uint8_t* smem
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + 8 * (2 * kW4MaxRing + buf));
-      buf ^= 1;
+      if (lane == 0) ptx::mbar_arrive(bars + 8 * (kW4BarSums + buf));
+      buf = (buf + 1) % kW4Bufs;
       if (buf == 0) taken ^= 1;
     }
     item += units;
@@ -298,7 +298,7 @@ __device__ __forceinline__ void w4_add_wide(const W4Stream& p, uint8_t* smem, co
   uint32_t there = 0;
   for (int part = 0; part < 2; ++part) {
     int lo, hi;
-    if (part == 1 && !job.plan([&] { return w4_wait(bars + 8 * (2 * kW4MaxRing + 4), 0, p, abort_flag); })) return;
+    if (part == 1 && !job.plan([&] { return w4_wait(bars + 8 * kW4BarPlan, 0, p, abort_flag); })) return;
     job.range(part, lo, hi);
     for (int item = lo; item < hi;) {
       const int slot = item / p.upe, first = item - slot * p.upe;
@@ -306,7 +306,7 @@ __device__ __forceinline__ void w4_add_wide(const W4Stream& p, uint8_t* smem, co
       const int sets = TERMS || n_rows <= 8 ? 1 : 2;
       for (int u0 = first; u0 < first + units; u0 += p.teams) {
         const int nb = min(p.teams, first + units - u0);
-        if (!w4_wait(bars + 8 * (2 * kW4MaxRing + buf), there, p, abort_flag)) return;
+        if (!w4_wait(bars + 8 * (kW4BarSums + buf), there, p, abort_flag)) return;
         for (int i = tid >> 5; i < nb * sets; i += kW4SumThreads / 32) {
           const int q = sets == 2 ? i >> 1 : i, n = sets == 2 ? i & 1 : 0;
           const float4* at = reinterpret_cast<const float4*>(sums_at + ((buf * p.teams + q) * p.kw) * 256 + n * 128);
@@ -321,8 +321,8 @@ __device__ __forceinline__ void w4_add_wide(const W4Stream& p, uint8_t* smem, co
           if (col + 1 < n_rows) job.store(slot, u0 + q, col + 1, mr, a.y, a.w);
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + 8 * (2 * kW4MaxRing + 2 + buf));
-        buf ^= 1;
+        if (lane == 0) ptx::mbar_arrive(bars + 8 * (kW4BarTaken + buf));
+        buf = (buf + 1) % kW4Bufs;
         if (buf == 0) there ^= 1;
       }
       item += units;
