@@ -6,16 +6,20 @@
 //   W[n][k] = (q[n][k] - z[n][k/G]) s[n][k/G],   z = 8 where there are no zero points.
 // A row's dot product is taken group by group: sum_g s[n][g] * (sum_{k in g} (q - z) x[k]).
 //
-// What bounds it is reading the codes once (K/2 bytes a row), if the instructions per byte
-// allow it: a SM gets 23 bytes of codes a clock, which leaves 88 clocks for 2 KB.  Made into
-// bf16 or fp16 operands of the tensor core, a word of 8 codes costs 9 to 11 instructions, and
-// the loop ran at half the memory's rate.  So the product runs in whole numbers: x goes, per
-// row and slice of 256 elements, into fixed point of 31 bits, taken apart into four signed
-// bytes, and mma.sync m16n8k32 (8-bit integers, 32-bit sums; per element of the reduction it
-// has twice the rate of the 16-bit form) multiplies code bytes with them, four columns a row
-// of x.  A word of codes costs 3 instructions, and a group's sum is exact.  Fixed point costs at most 2^-30 of the slice's largest |x| per element: nothing for
-// bf16 (fp16) elements down to 2^-22 (2^-19) of that, a quarter of fp32's own step on it
-// below.  The scale, and everything after it, is applied in fp32.
+// The floor is reading the codes once (K/2 bytes a row): 88 clocks of a SM for 2 KB at the
+// measured copy rate.  What bounds the loop is issuing instructions: made into bf16 or fp16
+// operands of the tensor core, a word of 8 codes costs 9 to 11, and 2 KB took 370 in all.  So
+// the product of a few rows of x runs in whole numbers: x goes, per row and slice of 256
+// elements, into fixed point of 31 bits, taken apart into four signed bytes, and mma.sync
+// m16n8k32 (8-bit integers, 32-bit sums; 2.1 clocks a SM, as the 16-bit m16n8k16 takes for half
+// the reduction) multiplies code bytes with them, four columns a row of x.  A word of codes
+// costs 3 instructions, 2 KB some 200, and a group's sum is exact.  Fixed point is off by at
+// most 2^-30 of the slice's largest |x| per element: nothing for bf16 (fp16) elements down to
+// 2^-22 (2^-19) of that, and below them less than a rounding of the largest to fp32.  The scale,
+// and everything after it, is applied in fp32.  More rows of x: w4_wide.cuh.
+//
+// Measured (device, CUDA graph of calls on three sets of data): 65536 x 4096, G = 128, 4 rows:
+// 36 us, 3.8 TB/s of 6.46, the 16-bit form 52 us; 4096 x 4096, 1 row: 6.0 us.
 //
 //   - a task is 16 rows x 256 reduction elements (2 KB of codes).  A warp keeps one slice of
 //     256 elements for all its tasks, so the B operand, up to 4 rows of x in that slice, sits
@@ -69,7 +73,7 @@ constexpr int kW4MaxWarps = 16;
 constexpr int kW4SetRows = 2;      // rows of x per B set: 4 bytes each fill the MMA's 8 columns
 constexpr int kW4Sets = 2;         // B sets of a warp
 constexpr int kW4Cols = kW4Sets * kW4SetRows;  // rows of x in a slot
-constexpr int kW4Batch = 2;        // units a team works on between two sums
+constexpr int kW4Batch = 2;        // units a team works on between two sums (1: 18% slower at 16 tokens; 3: 16%)
 constexpr int kW4Sums = 64 * kW4Sets;  // floats of a warp's sums of a unit
 
 // How a block's warps split the reduction: nchunk slices, `passes` rounds of kw warps; `teams`
@@ -87,10 +91,10 @@ inline W4Split w4_split(int K) {
   return s;
 }
 // Shared memory of a block of W consuming warps: the ring of codes (at a 1024-byte boundary),
-// of scales and of zero points, the buffers of partial sums, the sums of bytes of x, the barriers, the abort flag and a
-// counter; what the kernel adds comes after.
+// of scales and of zero points, the buffers of partial sums, the sums of bytes of x, the
+// barriers, the abort flag and a counter; what the kernel adds comes after.
 constexpr int kW4MaxRing = kW4Stages * kW4MaxWarps;  // most stages (one warp a unit)
-constexpr int kW4Bufs = 4;                           // buffers of partial sums
+constexpr int kW4Bufs = 4;                           // buffers of partial sums (2: 4% slower)
 constexpr int kW4PartBytes = 1024;                   // of a warp in one of them
 constexpr int kW4BarSums = 2 * kW4MaxRing, kW4BarTaken = kW4BarSums + kW4Bufs, kW4BarPlan = kW4BarTaken + kW4Bufs;
 constexpr int kW4ByteSums = 512;                     // of a warp's sums of x's bytes (two sets)

@@ -10,18 +10,20 @@
 //   kernel 2  routing and grouping again, down product, weighted sum (up to 8 tokens; with
 //             more a third, small one adds up)
 //
-// Both are w4_stream loops over (slot, unit) items, a slot being an expert with up to 4 of its
-// (token, choice) pairs, the shared expert's slots first, then the experts in ascending
-// order.  What bounds them is reading the active experts' codes once.  Every block works out
-// the routing and the slots for itself from the scores (one warp a token): that costs about
-// a microsecond in shared memory, where a kernel of its own would cost a launch and a round
-// trip through L2, and it lets kernel 2 start its weight copies before kernel 1 has
+// Both products are streams (w4.cuh) over (slot, unit) items, a slot being an expert with a few
+// of its (token, choice) pairs, the shared expert's slots first, then the experts.  The floor is
+// reading the active experts' codes once.  Every block works out the routing and the slots for
+// itself from the scores, one warp a token: that costs 2 to 5 us in shared memory, most of it
+// behind the first copies or kernel 1's last units, where a kernel of its own would cost a launch
+// and a round trip through L2, and it lets kernel 2 start its weight copies before kernel 1 has
 // finished.  The blocks' slots agree because pairs are ranked in (token, choice) order.
-// h stays fp32 in the workspace and enters the down product as x does the first two, as
-// 31-bit fixed point per 256 elements; in 16 bits it would leave 1.7e-3 (bf16) of relative
+// h stays fp32 in the workspace and enters the down product as x does the first two, with 30 or
+// 22 significant bits (w4.cuh, w4_wide.cuh); in 16 bits it would leave 1.7e-3 (bf16) of relative
 // error in an fp32 output.
-// The weighted sum of a few tokens runs where the last slot of 16 output rows finishes (an acq_rel count, as
-// in the single-token kernel), always in the order shared, j = 0..k-1.
+// Every sum has one order: slices, then y_shared and j = 0..k-1, so a call is deterministic.
+//
+// Measured (device, us; d = 4096, f = 2048, E = 256, k = 6, a shared expert, G = 128): 1 token 39
+// (2.3 TB/s), 16 tokens 210, 64 tokens 566, both with Zipf(1) routing.
 #pragma once
 #include <type_traits>
 

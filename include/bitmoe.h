@@ -275,8 +275,11 @@ int moe_shared_expert_fp8(const uint16_t* x_bf16, int T, const moe_fp8_expert_t*
  *   scales [N][K/G] bf16 or fp16, the activations' type; 2-byte aligned
  *   zeros  [N][K/G] uint8, 0..127 (the low seven bits are read), or NULL: 8 everywhere
  *   W[n][k] = (q[n][k] - zeros[n][k/G]) * scales[n][k/G].
- * Activations stay in 16 bits: products are exact, a group's sum and everything after it is
- * fp32. */
+ * Activations are not quantised.  A few rows enter the product as 31-bit fixed point per 256
+ * elements (off by at most 2^-30 of the largest of them: nothing for elements of 2^-19 of it
+ * and more), more rows in their 16 bits; a group's sum is exact or fp32, the scale and everything
+ * after it fp32.  An infinity or NaN in a row gives what floating point gives, in that row
+ * alone. */
 typedef struct {
   const uint8_t* codes;
   const void* scales;
@@ -291,7 +294,8 @@ typedef struct {
  *   x [M][K] bf16 or fp16 bit patterns (`dtype`; the scales have the same type), 16-byte
  *   aligned; C [M][N] fp32 out, 4-byte aligned.
  * 0 <= M <= 64; K a positive multiple of group, at most 2^20; 1 <= N <= 2^24.  One kernel, no
- * workspace.  Rows of x do not meet: a row's result does not depend on the others. */
+ * workspace.  Rows of x do not meet: at the same M, a row's result does not depend on the
+ * others. */
 int moe_w4_gemm(const void* x, int dtype, int M, const moe_w4_matrix_t* w, int N, int K,
                 int group, float* C, void* stream);
 
@@ -310,16 +314,16 @@ typedef struct {
   int shared;
 } moe_w4_weights_t;
 
-/* moe_forward on 4-bit weights with group scales, for a few tokens, in two kernels: the top-k
- * of the scores, g = W_gate x, u = W_up x, h = silu(g) * u, y = W_down h for every selected
- * expert and the shared one, and out[t] = y_shared[t] + sum_j topk_w[t,j] y[t,j].
+/* moe_forward on 4-bit weights with group scales, for a few tokens, in two kernels (three above
+ * 8 tokens): the top-k of the scores, g = W_gate x, u = W_up x, h = silu(g) * u, y = W_down h
+ * for every selected expert and the shared one, and out[t] = y_shared[t] + sum_j topk_w[t,j] y[t,j].
  *   scores, topk_idx, topk_w, out as for moe_forward; x [T][d] of w->dtype, 16-byte aligned.
  *   ws: at least moe_w4_workspace_size(T, k, E, d, f, shared) bytes, 256-byte aligned; its
  *   contents need not be initialised.  Calls that may overlap on the GPU (other streams,
  *   graphs replayed side by side) need a workspace each.
- * 0 <= T <= 64; 1 <= k <= min(E, 32); 1 <= E <= 1024.  h enters the second product with
- * 22 significant bits (and at least 2^-39 of the largest h of its 256 elements).  A call is
- * deterministic. */
+ * 0 <= T <= 64; 1 <= k <= min(E, 32); 1 <= E <= 1024.  h enters the second product with 22
+ * significant bits or more (or off by at most 2^-30 of the largest h of its 256 elements).  A
+ * call is deterministic. */
 int moe_forward_w4(const float* scores, const void* x, int T, int k, const moe_w4_weights_t* w,
                    int32_t* topk_idx, float* topk_w, float* out, void* ws, size_t ws_bytes,
                    void* stream);
