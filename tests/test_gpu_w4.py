@@ -266,7 +266,10 @@ LAYERS = [  # T, E, k, d, f, G, dtype, zeros, shared
     (16, 4, 2, 1088, 832, 64, FP, True, True), (17, 1024, 4, 96, 64, 32, BF, True, True),
     (33, 600, 32, 128, 256, 64, FP, False, True), (64, 8, 1, 4224, 384, 128, BF, True, False),
     (64, 128, 6, 1024, 512, 128, BF, False, True), (64, 40, 32, 64, 64, 32, FP, True, True),
-    (12, 6, 2, 256, 4352, 128, FP, False, True)]
+    (12, 6, 2, 256, 4352, 128, FP, False, True), (3, 1024, 8, 256, 256, 128, BF, True, False),
+    (4, 300, 8, 1024, 512, 32, FP, False, True), (2, 600, 32, 192, 320, 64, BF, False, True),
+    (1, 64, 32, 512, 2048, 64, FP, True, False), (64, 1, 1, 256, 128, 32, BF, False, False),
+    (10, 2, 2, 4608, 96, 32, FP, True, True)]
 
 
 @pytest.mark.parametrize("T,E,k,d,f,G,dtype,zeros,shared", LAYERS)
@@ -280,6 +283,37 @@ def test_layer(T, E, k, d, f, G, dtype, zeros, shared):
     bm.sync_status()
     worst, rel = check_layer_w4(r, x, s, k, mats, shared, G)
     print(f"W4LAYER T={T} E={E} k={k} d={d} f={f} G={G}: worst err/bound {worst:.2e}, rel {rel:.2e}")
+
+
+def test_layer_without_tokens():
+    _, w = make_layer(4, 4, 64, 64, 32, BF, False, True)
+    r = bm.forward_w4(torch.empty((0, 64), dtype=BF, device="cuda"), torch.empty((0, 4), device="cuda"), 2, w)
+    bm.sync_status()
+    assert r["out"].shape == (0, 64) and r["idx"].shape == (0, 2)
+
+
+def test_refusals_on_the_gpu():
+    """A misaligned x, a workspace too small, too many tokens and k above E come back as errors."""
+    E, d, f, G = 4, 64, 64, 32
+    _, w = make_layer(4, E, d, f, G, BF, False, True)
+    x, s = torch.zeros((3, d), dtype=BF, device="cuda"), torch.zeros((3, E), device="cuda")
+    off = torch.zeros(3 * d + 1, dtype=BF, device="cuda")[1:].view(3, d)
+    m = bm.W4Matrix(w.gate.codes[0], w.gate.scales[0])
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for code, call in [(bm.MOE_ERR_INVALID_ARG, lambda: bm.w4_gemm(off, m)),
+                       (bm.MOE_ERR_INVALID_ARG, lambda: bm.w4_gemm(x[:1].expand(65, d).contiguous(), m)),
+                       (bm.MOE_ERR_INVALID_ARG, lambda: bm.forward_w4(off, s, 2, w)),
+                       (bm.MOE_ERR_INVALID_ARG, lambda: bm.forward_w4(x, s, 5, w)),
+                       (bm.MOE_ERR_WORKSPACE, lambda: bm.forward_w4(x, s, 2, w, ws=ws))]:
+        with pytest.raises(bm.MoeError) as ei:
+            call()
+        assert ei.value.code == code
+    for call in (lambda: bm.w4_gemm(x.t().contiguous().t(), m), lambda: bm.w4_gemm(x.half(), m),
+                 lambda: bm.forward_w4(x, s.t().contiguous().t(), 2, w),
+                 lambda: bm.forward_w4(x, s, 2, w, outs={"out": torch.empty((3, d + 1), device="cuda")})):
+        with pytest.raises(ValueError):
+            call()
+    bm.sync_status()
 
 
 @pytest.mark.parametrize("T", [1, 8, 9, 64])
