@@ -455,7 +455,8 @@ __device__ __noinline__ float w4_slow_dot(const typename T::Raw* x, const uint8_
 // being an expert (or the matrix) with up to kW4Cols rows of x, a unit 16 rows of the matrix, or
 // 8 rows of the first matrix and the same 8 of the second (DUAL).  Job supplies the slots and
 // takes the sums:
-//   range(part, lo, hi)     the block's items, in two parts [lo, hi)
+//   range(part, lo, hi)     the block's items, in two parts [lo, hi); kLastPart: the last that
+//                           can hold any
 //   matrix(slot)            the slot's matrix (its rows start at matrix * rows)
 //   plan(wait)              called by every warp before part 1; wait() is true once the slots are
 //                           known (false if a wait has run out)
@@ -484,7 +485,7 @@ __device__ __forceinline__ void w4_init(const W4Stream& p, uint8_t* smem, const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kW4Bufs; ++i) {
       ptx::mbar_init(bars + 8 * (kW4BarSums + i), L.warps);                 // sums there
-      ptx::mbar_init(bars + 8 * (kW4BarTaken + i), kW4SumThreads / 32);  // sums taken
+      ptx::mbar_init(bars + 8 * (kW4BarTaken + i), 1);         // sums taken
     }
     ptx::mbar_init(bars + 8 * kW4BarPlan, 1);  // the slots are known
     *reinterpret_cast<int*>(smem + L.abort_flag()) = 0;
@@ -493,8 +494,7 @@ __device__ __forceinline__ void w4_init(const W4Stream& p, uint8_t* smem, const 
   ptx::fence_mbar_init();
 }
 // A wait of a whole warp: true once the phase is complete, false if a wait has run out.  The
-// warp is parked by the hardware for most of it: warps that poll (one of the copying and
-// adding warps sits on each of the SM's partitions) took half of the issue slots.
+// hardware may park the warp for most of it (polling it takes the same times).
 __device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, const W4Stream& p, volatile int* abort_flag) {
   constexpr uint32_t kPark = 20000;  // ns
   if (__all_sync(0xffffffffu, ptx::mbar_try_wait_for(bar, parity, p.wait_ns < kPark ? (uint32_t)p.wait_ns : kPark)))
@@ -739,13 +739,14 @@ __device__ __forceinline__ void w4_consume(const W4Stream& p, uint8_t* smem, con
   }
 }
 
-// The adding warps: the consuming warps' sums of a batch, a warp a unit.  A row of x has two
+// The adding warps take the batches of the consuming warps' sums in turn.  A row of x has two
 // lanes of a quad, its low and its high bytes.  Lane (sub, r) takes every fourth slice of row
 // pair r, for each row of x; the four of a row pair join what they have, and lane group `sub`
 // stores row `sub` of x.  `tid`: 0 .. kW4SumThreads - 1.
 template <typename T, typename S, int G, bool ZP, bool RING, bool DUAL, typename Job>
 __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const Job& job, int tid) {
   constexpr int ROWS = DUAL ? 8 : kW4Rows;
+  int turn = tid >> 5;  // batches until the warp's next
   const int r = tid & 7, sub = (tid >> 3) & 3, mr = w4_row<G>(r);
   const int UB = kW4Batch * p.teams, ngr = p.K / G;
   const W4Smem L = w4_smem<G, ZP, RING>(p);
@@ -763,8 +764,10 @@ __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const J
       const int units = min(p.upe - first, hi - item), n_rows = job.rows(slot);
       for (int u0 = first; u0 < first + units; u0 += UB) {
         const int nb = min(UB, first + units - u0);
-        if (!w4_wait(bars + 8 * (kW4BarSums + buf), there, p, abort_flag)) return;
-        for (int q = tid >> 5; q < nb; q += kW4SumThreads / 32) {
+        const bool last = part == Job::kLastPart && item + units >= hi && u0 + UB >= first + units;
+        const bool mine = turn == 0 || last;  // all three share the last batch
+        if (mine && !w4_wait(bars + 8 * (kW4BarSums + buf), there, p, abort_flag)) return;
+        for (int q = last ? tid >> 5 : 0; q < nb && mine; q += last ? kW4SumThreads / 32 : 1) {
           const float4* at = reinterpret_cast<const float4*>(sums_at + (buf * UB + q) * p.kw * kW4Sums + r * 8);
           float a = 0.f, b = 0.f;  // of column `sub`
 #pragma unroll
@@ -798,7 +801,8 @@ __device__ __forceinline__ void w4_add(const W4Stream& p, uint8_t* smem, const J
           job.store(slot, unit, sub, mr, a, b);
         }
         __syncwarp();
-        if ((tid & 31) == 0) ptx::mbar_arrive(bars + 8 * (kW4BarTaken + buf));
+        if ((tid & 31) == 0 && turn == 0 && !last) ptx::mbar_arrive(bars + 8 * (kW4BarTaken + buf));
+        turn = turn == 0 ? kW4SumThreads / 32 - 1 : turn - 1;
         buf = (buf + 1) % kW4Bufs;
         if (buf == 0) there ^= 1;
       }

@@ -29,6 +29,7 @@ struct W4GemmParams {
 template <int COLS>
 struct GemmJob {
   const W4GemmParams& p;
+  static constexpr int kLastPart = 0;
   __device__ __forceinline__ void range(int part, int& lo, int& hi) const {
     const unsigned total = (unsigned)(p.slots * p.st.upe);  // below 2^23: 32 bits hold the products
     lo = part == 0 ? (int)(blockIdx.x * total / gridDim.x) : 0;

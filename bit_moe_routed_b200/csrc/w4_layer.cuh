@@ -224,6 +224,7 @@ struct LayerJob {
   W4Plan L;
   uint8_t* scratch;  // for w4_plan_few
   uint32_t ready;    // barrier: the slots are known
+  static constexpr int kLastPart = 1;
   // at most 2^22 items: 32 bits hold the products
   __device__ __forceinline__ void whole_range(int part, int& lo, int& hi) const {
     lo = hi = 0;

@@ -285,11 +285,12 @@ __device__ __forceinline__ void w4_consume_wide(const W4Stream& p, uint8_t* smem
   }
 }
 
-// The adding warps: (unit, set) by (unit, set), a lane of theirs for a lane of the MMA.
+// The adding warps take the batches in turn, a lane of theirs for a lane of the MMA.
 template <typename T, int G, bool ZP, bool RING, bool DUAL, typename Job>
 __device__ __forceinline__ void w4_add_wide(const W4Stream& p, uint8_t* smem, const Job& job, int tid) {
   constexpr bool TERMS = sizeof(typename T::Raw) == 4;
   const int lane = tid & 31, g = lane >> 2, t = lane & 3;
+  int turn = tid >> 5;  // batches until the warp's next
   const W4Smem L = w4_smem<G, ZP, RING>(p);
   const uint32_t bars = ptx::smem_u32(smem + L.bars());
   const float* const sums_at = reinterpret_cast<const float*>(smem + L.part()) + lane * 4;
@@ -306,8 +307,10 @@ __device__ __forceinline__ void w4_add_wide(const W4Stream& p, uint8_t* smem, co
       const int sets = TERMS || n_rows <= 8 ? 1 : 2;
       for (int u0 = first; u0 < first + units; u0 += p.teams) {
         const int nb = min(p.teams, first + units - u0);
-        if (!w4_wait(bars + 8 * (kW4BarSums + buf), there, p, abort_flag)) return;
-        for (int i = tid >> 5; i < nb * sets; i += kW4SumThreads / 32) {
+        const bool last = part == Job::kLastPart && item + units >= hi && u0 + p.teams >= first + units;
+        const bool mine = turn == 0 || last;  // all three share the last batch
+        if (mine && !w4_wait(bars + 8 * (kW4BarSums + buf), there, p, abort_flag)) return;
+        for (int i = last ? tid >> 5 : 0; i < nb * sets && mine; i += last ? kW4SumThreads / 32 : 1) {
           const int q = sets == 2 ? i >> 1 : i, n = sets == 2 ? i & 1 : 0;
           const float4* at = reinterpret_cast<const float4*>(sums_at + ((buf * p.teams + q) * p.kw) * 256 + n * 128);
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -321,7 +324,8 @@ __device__ __forceinline__ void w4_add_wide(const W4Stream& p, uint8_t* smem, co
           if (col + 1 < n_rows) job.store(slot, u0 + q, col + 1, mr, a.y, a.w);
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + 8 * (kW4BarTaken + buf));
+        if (lane == 0 && turn == 0 && !last) ptx::mbar_arrive(bars + 8 * (kW4BarTaken + buf));
+        turn = turn == 0 ? kW4SumThreads / 32 - 1 : turn - 1;
         buf = (buf + 1) % kW4Bufs;
         if (buf == 0) there ^= 1;
       }
