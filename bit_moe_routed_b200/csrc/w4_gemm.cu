@@ -14,7 +14,7 @@ namespace {
 
 // Up to 4 rows of x take the whole-number form, more the 16-bit one, 16 rows a slot.  Both, in us
 // (8192 x 4096, G = 128, bf16): 1 row 7.3 and 10.2, 4 rows 9.5 and 10.6, 5 rows 12.6 and 11.0,
-// 16 rows 19.5 and 15.0, 64 rows 62 and 35.
+// 16 rows 19.5 and 15.0, 64 rows 62 and 32.
 constexpr int kW4WholeRows = 4;
 constexpr int kW4WideRows = 16;
 

@@ -5,7 +5,7 @@ namespace bitmoe {
 namespace {
 
 // Whether a call takes the 16-bit form: where an expert has four pairs and more on average (32
-// tokens, 16 experts, k = 4, d = 2048, f = 1408: 90 us against 121 in whole numbers).
+// tokens, 16 experts, k = 4, d = 2048, f = 1408: 87 us against 121 in whole numbers).
 bool w4_wide(int T, int k, int E) { return T > 8 && T * k >= 4 * E; }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }

@@ -22,8 +22,8 @@
 // error in an fp32 output.
 // Every sum has one order: slices, then y_shared and j = 0..k-1, so a call is deterministic.
 //
-// Measured (device, us; d = 4096, f = 2048, E = 256, k = 6, a shared expert, G = 128): 1 token 39
-// (2.3 TB/s), 16 tokens 210, 64 tokens 566, both with Zipf(1) routing.
+// Measured (device, us; d = 4096, f = 2048, E = 256, k = 6, a shared expert, G = 128): 1 token 40
+// (2.3 TB/s), 16 tokens 202, 64 tokens 540, both with Zipf(1) routing.
 #pragma once
 #include <type_traits>
 
@@ -55,9 +55,9 @@ namespace {
 
 // The slots in shared memory: up to sc pairs, the expert and the count of each; the
 // pairs' weights.  The shared expert's slots, the first, are known without them: slot s has
-// tokens s sc and up.
+// tokens s * sc and up.
 struct W4Plan {
-  uint16_t* pair;  // [slots][kW4Cols]
+  uint16_t* pair;  // [slots][sc]
   int16_t* e;
   uint8_t* n;
   float* w;        // [P]
